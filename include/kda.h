@@ -40,8 +40,8 @@
  *     tolerances, about 20 % slower); kda_last_prefill_path tells which ran.
  *   - the fixed array of KDA_NOALLOC_SCRATCH_BYTES behind
  *     kda_prefill_noalloc, present on every device that loads the library.
- * kda_prefill_ws, kda_prefill_at, the decode and backward calls and the
- * affine maps take no device memory of their own.
+ * kda_prefill_ws, kda_prefill_at, the decode, tree, verification, cache and
+ * backward calls and the affine maps take no device memory of their own.
  *
  * Errors: argument problems return KDA_ERR_INVALID_ARGUMENT or
  * KDA_ERR_UNSUPPORTED before anything is launched.  A failed launch returns
@@ -71,6 +71,9 @@ typedef enum {
 } kda_status;
 
 typedef enum { KDA_DTYPE_F32 = 0, KDA_DTYPE_BF16 = 1 } kda_dtype;
+
+/* Element type of an 8-bit state cache (kda_state_store). */
+typedef enum { KDA_CACHE_E4M3 = 0, KDA_CACHE_INT8 = 1 } kda_cache_dtype;
 
 typedef struct {
   int32_t num_seqs;     /* N >= 1                                                  */
@@ -234,13 +237,119 @@ kda_status kda_decode(const void *q, const void *k, const void *v, const float *
  * D_k = D_v = 128 and at most 16 tokens compute it as one chunk of the
  * chunked form (Methods 1, FlashKDA) on the tensor cores, with S0 rounded to
  * BF16 as an operand and the state updated in FP32; other shapes run the
- * recurrence on the CUDA cores.  The serving side that decides acceptance is
- * not part of this library.
+ * recurrence on the CUDA cores.  kda_verify_tree decides acceptance: its
+ * accept_len output is this call's accept_len input.
  */
 kda_status kda_decode_multi(const void *q, const void *k, const void *v, const float *g,
                             const float *beta, float *state_inout, void *out,
                             const int32_t *accept_len, int32_t tokens_per_seq,
                             const kda_shape *shape, kda_stream_t stream);
+
+/*
+ * Trees of drafted tokens.  A sequence brings nodes_per_seq places; place i
+ * holds a drafted token whose predecessor is place parents[n][i] < i, or the
+ * committed state for -1.  Any other value (i or larger, below -1) marks an
+ * empty place: sequences with fewer tokens fill their rows up with -2.  A token
+ * whose path to the state holds an empty place is itself empty.  parents may be
+ * NULL: place i follows place i - 1 (a chain).  One round of speculative
+ * decoding is kda_decode_tree in every layer, kda_verify_tree on the
+ * probabilities, and kda_tree_commit in every layer.
+ *
+ * kda_decode_tree: the output of every token, as if the recurrence had run from
+ * state along the token's path ("LLM - Semianalysis, Kimi K3 아키텍처"
+ * (charstring.tistory.com/2557), Methods 1: decode runs the recurrence
+ * directly).  state is only read.  The tree is computed as one chunk of the
+ * chunked form whose causal mask is "is an ancestor of".
+ *
+ *   q, k, g : [N, nodes_per_seq, H, D_k]   v, out : [N, nodes_per_seq, H, D_v]
+ *   beta    : [N, nodes_per_seq, H]         state  : [N, H, D_k, D_v] FP32
+ *   parents : device int32[N, nodes_per_seq] or NULL
+ * Rows of out at empty places are zero; what q, k, v, g and
+ * beta hold there does not matter.  FP32 inputs give FP32
+ * accuracy; BF16 inputs run the products in TF32, below the rounding of out.
+ *
+ * kda_tree_commit: state_out = the state after place accept_node[n], by the
+ * recurrence in FP32 along its path.  A value outside [0, nodes_per_seq), or an
+ * empty place, accepts nothing: state_out = state.  state_out may be state (in
+ * place), but must not partly overlap it.
+ *   accept_node : device int32[N]; other arguments as above.
+ *
+ * shape->total_tokens must equal N * nodes_per_seq; 1 <= nodes_per_seq <= 64;
+ * shape->chunk and shape->dev_status are ignored.
+ */
+kda_status kda_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, const float *state, const int32_t *parents,
+                           void *out, int32_t nodes_per_seq, const kda_shape *shape,
+                           kda_stream_t stream);
+kda_status kda_tree_commit(const void *k, const void *v, const float *g, const float *beta,
+                           const float *state, float *state_out, const int32_t *parents,
+                           const int32_t *accept_node, int32_t nodes_per_seq,
+                           const kda_shape *shape, kda_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given
+ * random numbers: accepted and drawn tokens together follow the target's
+ * distribution.  For a context c (the committed prefix, or a place) let p_c and
+ * d_c be the target's and the draft's distribution after it, and start with
+ * c = prefix, r = p_c, R = 1.  Successors of c are tried in the order of their
+ * places; token x at place i is accepted when r(x) > 0 and
+ * u_i R d_c(x) < r(x).  Accepted: c = i, r = p_c, R = 1.  Refused:
+ * r = max(r / R - d_c, 0), R = sum(r).  When c has no successor left the next
+ * token is the smallest j with r(0) + ... + r(j) > u_last sum(r) (if r is zero
+ * everywhere, the same with r = p_c).  Sums and comparisons are FP64.
+ *
+ *   target_probs : [N, nodes_per_seq + 1, vocab]; row 0 is p after the prefix,
+ *                  row i + 1 after place i.  Each row sums to one.
+ *   draft_probs  : [N, nodes_per_seq, vocab]; row 0 is d after the prefix, row
+ *                  i + 1 after place i, so that of a chain row i is what place
+ *                  i was drawn from.  NULL: tokens that were not drawn but
+ *                  looked up; d_c is then one at the token tried, a refusal
+ *                  sets r(x) = 0 and R = R - r(x).
+ *   tokens       : int32[N, nodes_per_seq]; outside [0, vocab): probability 0.
+ *   parents      : int32[N, nodes_per_seq] as for kda_decode_tree, or NULL.
+ *   uniforms     : FP32[N, nodes_per_seq + 1] in [0, 1): one per place, and
+ *                  u_last for the token drawn at the end.
+ *   accept_node  : int32[N], the last accepted place, -1 for none.
+ *   accept_len   : int32[N], the number of accepted tokens.
+ *   out_tokens   : int32[N, nodes_per_seq + 1]: the accepted tokens, the drawn
+ *                  one (-1 if its row holds no probability at all), then -1.
+ * Probabilities are FP32 or BF16 (prob_dtype, a kda_dtype), non-negative and
+ * finite; rows need no more alignment than their elements (rows of a multiple
+ * of 16 bytes are read fastest).  All pointers are device pointers.
+ * vocab <= 2^30, num_seqs <= 2^27, 1 <= nodes_per_seq <= 64.
+ */
+kda_status kda_verify_tree(const void *target_probs, const void *draft_probs,
+                           const int32_t *tokens, const int32_t *parents, const float *uniforms,
+                           int32_t *accept_node, int32_t *accept_len, int32_t *out_tokens,
+                           int32_t num_seqs, int32_t nodes_per_seq, int64_t vocab,
+                           int32_t prob_dtype, kda_stream_t stream);
+
+/*
+ * The 8-bit state cache: a pool of num_slots states for prefix caching, a
+ * quarter of the FP32 size.  Each row (key channel) of a state has one FP32
+ * scale, its largest magnitude over the code type's largest value (448 for E4M3,
+ * 127 for INT8); a code is the element over the scale, rounded to nearest even.
+ * Rows of zeros store zeros; a row that holds an infinity or a NaN reads back as
+ * NaN.
+ *
+ * kda_state_store writes states[i] to slot slots[i]; a value outside
+ * [0, num_slots) is skipped, and of several entries with one slot the last
+ * stays.  kda_state_load reads states[i] from slot slots[i]; a value outside
+ * [0, num_slots) gives the zero state.
+ *
+ *   states : [N, H, D_k, D_v] FP32      slots  : device int32[N]
+ *   cache  : [num_slots, H, D_k, D_v] bytes (cache_dtype, a kda_cache_dtype)
+ *   scales : [num_slots, H, D_k] FP32
+ * N, H, D_k and D_v come from the shape (num_seqs, ...); its other fields are
+ * checked but not used.  states, cache and scales must be 16-byte aligned; no
+ * two arguments may overlap.
+ */
+kda_status kda_state_store(const float *states, const int32_t *slots, void *cache, float *scales,
+                           int64_t num_slots, int32_t cache_dtype, const kda_shape *shape,
+                           kda_stream_t stream);
+kda_status kda_state_load(const void *cache, const float *scales, const int32_t *slots,
+                          float *states, int64_t num_slots, int32_t cache_dtype,
+                          const kda_shape *shape, kda_stream_t stream);
 
 /*
  * Backward pass of the recurrence, for training (the pages name training work

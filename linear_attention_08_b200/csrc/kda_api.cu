@@ -21,6 +21,23 @@ cudaError_t launch_decode_multi(int dtype, int dk, int dv, const void *q, const 
                                 const void *v, const float *g, const float *beta, float *state,
                                 void *out, const int32_t *accept_len, int T_new, int64_t units,
                                 int H, int32_t *dev_status, cudaStream_t stream);
+cudaError_t launch_decode_tree(int dtype, int dk, int dv, const void *q, const void *k,
+                               const void *v, const float *g, const float *beta,
+                               const float *state, const int32_t *parents, void *out, int T,
+                               int64_t units, int H, cudaStream_t stream);
+cudaError_t launch_tree_commit(int dtype, int dk, int dv, const void *k, const void *v,
+                               const float *g, const float *beta, const float *state,
+                               float *state_out, const int32_t *parents,
+                               const int32_t *accept_node, int T, int64_t units, int H,
+                               cudaStream_t stream);
+cudaError_t launch_verify_tree(bool bf16, const void *target, const void *draft,
+                               const int32_t *tokens, const int32_t *parents,
+                               const float *uniforms, int32_t *accept_node, int32_t *accept_len,
+                               int32_t *out_tokens, int N, int T, int vocab, int num_sms,
+                               cudaStream_t stream);
+cudaError_t launch_state_cache(bool store, bool e4m3, int dk, int dv, float *states,
+                               const int32_t *slots, void *cache, float *scales, int N, int H,
+                               int64_t num_slots, cudaStream_t stream);
 bool prefill_tc_supported(int dtype, int dk, int dv, int chunk);
 cudaError_t launch_prefill_tc(const void *q, const void *k, const void *v, const float *g,
                               const float *beta, const float *init, const int32_t *cu,
@@ -179,6 +196,11 @@ static kda_status cuda_status(cudaError_t e) {
 }
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Places of a tree of drafted tokens (and of a draft, kda_decode_multi).
+constexpr int kMaxTreeNodes = 64;
 
 static bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
@@ -566,6 +588,150 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const f
                                          beta, state_inout, out, accept_len, tokens_per_seq,
                                          units, s->num_heads, s->dev_status,
                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, const float *state, const int32_t *parents,
+                           void *out, int32_t nodes_per_seq, const kda_shape *s,
+                           kda_stream_t stream) {
+  kda_status st = check_shape(s, false);
+  if (st != KDA_OK) return st;
+  if (nodes_per_seq < 1 || nodes_per_seq > kMaxTreeNodes) return KDA_ERR_INVALID_ARGUMENT;
+  if (s->total_tokens != (int64_t)s->num_seqs * nodes_per_seq) return KDA_ERR_INVALID_ARGUMENT;
+  const void *ptrs[] = {q, k, v, g, state, out};
+  for (const void *p : ptrs)
+    if (!p || !aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!beta || !aligned4(beta) || !aligned4(parents)) return KDA_ERR_INVALID_ARGUMENT;
+  const int64_t units = (int64_t)s->num_seqs * s->num_heads;
+  const int64_t T = s->total_tokens, H = s->num_heads;
+  const size_t es = elem_size(s->qkv_dtype);
+  const size_t n_qk = (size_t)T * H * s->head_dim_k * es, n_g = (size_t)T * H * s->head_dim_k * 4;
+  const size_t n_out = (size_t)T * H * s->head_dim_v * es;
+  const size_t n_state = (size_t)units * s->head_dim_k * s->head_dim_v * 4;
+  if (overlaps(out, n_out, state, n_state) || overlaps(out, n_out, q, n_qk) ||
+      overlaps(out, n_out, k, n_qk) || overlaps(out, n_out, v, n_out) ||
+      overlaps(out, n_out, g, n_g) || overlaps(out, n_out, beta, (size_t)T * H * 4) ||
+      overlaps(out, n_out, parents, (size_t)T * 4))
+    return KDA_ERR_INVALID_ARGUMENT;
+  return cuda_status(launch_decode_tree(s->qkv_dtype, s->head_dim_k, s->head_dim_v, q, k, v, g,
+                                        beta, state, parents, out, nodes_per_seq, units,
+                                        s->num_heads, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_tree_commit(const void *k, const void *v, const float *g, const float *beta,
+                           const float *state, float *state_out, const int32_t *parents,
+                           const int32_t *accept_node, int32_t nodes_per_seq, const kda_shape *s,
+                           kda_stream_t stream) {
+  kda_status st = check_shape(s, false);
+  if (st != KDA_OK) return st;
+  if (nodes_per_seq < 1 || nodes_per_seq > kMaxTreeNodes) return KDA_ERR_INVALID_ARGUMENT;
+  if (s->total_tokens != (int64_t)s->num_seqs * nodes_per_seq) return KDA_ERR_INVALID_ARGUMENT;
+  const void *ptrs[] = {k, v, g, state, state_out};
+  for (const void *p : ptrs)
+    if (!p || !aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!beta || !aligned4(beta) || !aligned4(parents) || !accept_node || !aligned4(accept_node))
+    return KDA_ERR_INVALID_ARGUMENT;
+  const int64_t units = (int64_t)s->num_seqs * s->num_heads;
+  const int64_t T = s->total_tokens, H = s->num_heads;
+  const size_t es = elem_size(s->qkv_dtype);
+  const size_t n_state = (size_t)units * s->head_dim_k * s->head_dim_v * 4;
+  // in place is fine (each CTA reads its unit before it writes it), a partial overlap is not
+  if ((state_out != state && overlaps(state_out, n_state, state, n_state)) ||
+      overlaps(state_out, n_state, k, (size_t)T * H * s->head_dim_k * es) ||
+      overlaps(state_out, n_state, v, (size_t)T * H * s->head_dim_v * es) ||
+      overlaps(state_out, n_state, g, (size_t)T * H * s->head_dim_k * 4) ||
+      overlaps(state_out, n_state, beta, (size_t)T * H * 4) ||
+      overlaps(state_out, n_state, parents, (size_t)T * 4) ||
+      overlaps(state_out, n_state, accept_node, (size_t)s->num_seqs * 4))
+    return KDA_ERR_INVALID_ARGUMENT;
+  return cuda_status(launch_tree_commit(s->qkv_dtype, s->head_dim_k, s->head_dim_v, k, v, g, beta,
+                                        state, state_out, parents, accept_node, nodes_per_seq,
+                                        units, s->num_heads,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_verify_tree(const void *target_probs, const void *draft_probs,
+                           const int32_t *tokens, const int32_t *parents, const float *uniforms,
+                           int32_t *accept_node, int32_t *accept_len, int32_t *out_tokens,
+                           int32_t num_seqs, int32_t nodes_per_seq, int64_t vocab,
+                           int32_t prob_dtype, kda_stream_t stream) {
+  if (num_seqs < 1 || nodes_per_seq < 1 || nodes_per_seq > kMaxTreeNodes || vocab < 1)
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (prob_dtype != KDA_DTYPE_F32 && prob_dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARGUMENT;
+  if (vocab > ((int64_t)1 << 30) || num_seqs > ((int32_t)1 << 27)) return KDA_ERR_UNSUPPORTED;
+  const size_t es = elem_size(prob_dtype);
+  const void *ints[] = {tokens, uniforms, accept_node, accept_len, out_tokens};
+  for (const void *p : ints)
+    if (!p || !aligned4(p)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!aligned4(parents)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!target_probs || (reinterpret_cast<uintptr_t>(target_probs) & (es - 1)) ||
+      (reinterpret_cast<uintptr_t>(draft_probs) & (es - 1)))
+    return KDA_ERR_INVALID_ARGUMENT;
+  const size_t N = (size_t)num_seqs, T = (size_t)nodes_per_seq, V = (size_t)vocab;
+  const void *outs[] = {accept_node, accept_len, out_tokens};
+  const size_t out_n[] = {N * 4, N * 4, N * (T + 1) * 4};
+  const void *ins[] = {target_probs, draft_probs, tokens, parents, uniforms};
+  const size_t in_n[] = {N * (T + 1) * V * es, N * T * V * es, N * T * 4, N * T * 4,
+                         N * (T + 1) * 4};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (overlaps(outs[i], out_n[i], ins[j], in_n[j])) return KDA_ERR_INVALID_ARGUMENT;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlaps(outs[i], out_n[i], outs[j], out_n[j])) return KDA_ERR_INVALID_ARGUMENT;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  return cuda_status(launch_verify_tree(prob_dtype == KDA_DTYPE_BF16, target_probs, draft_probs,
+                                        tokens, parents, uniforms, accept_node, accept_len,
+                                        out_tokens, num_seqs, nodes_per_seq, (int)vocab,
+                                        device_sms(dev), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Arguments of the cache calls that store and load share.
+static kda_status check_cache(const float *states, const int32_t *slots, const void *cache,
+                              const float *scales, int64_t num_slots, int32_t cache_dtype,
+                              const kda_shape *s) {
+  kda_status st = check_shape(s, false);
+  if (st != KDA_OK) return st;
+  if (cache_dtype != KDA_CACHE_E4M3 && cache_dtype != KDA_CACHE_INT8) return KDA_ERR_INVALID_ARGUMENT;
+  if (num_slots < 1) return KDA_ERR_INVALID_ARGUMENT;
+  // slots are int32; 2^40 (slot, head) pairs keep the byte counts below in 64 bits
+  if (num_slots > INT32_MAX || num_slots * s->num_heads > ((int64_t)1 << 40)) return KDA_ERR_UNSUPPORTED;
+  const void *ptrs[] = {states, cache, scales};
+  for (const void *p : ptrs)
+    if (!p || !aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!slots || !aligned4(slots)) return KDA_ERR_INVALID_ARGUMENT;
+  const int H = s->num_heads, DK = s->head_dim_k, DV = s->head_dim_v;
+  const size_t n_state = (size_t)s->num_seqs * H * DK * DV * 4;
+  const size_t n_cache = (size_t)num_slots * H * DK * DV, n_scale = (size_t)num_slots * H * DK * 4;
+  const size_t n_slots = (size_t)s->num_seqs * 4;
+  if (overlaps(states, n_state, cache, n_cache) || overlaps(states, n_state, scales, n_scale) ||
+      overlaps(cache, n_cache, scales, n_scale) || overlaps(slots, n_slots, states, n_state) ||
+      overlaps(slots, n_slots, cache, n_cache) || overlaps(slots, n_slots, scales, n_scale))
+    return KDA_ERR_INVALID_ARGUMENT;
+  return KDA_OK;
+}
+
+kda_status kda_state_store(const float *states, const int32_t *slots, void *cache, float *scales,
+                           int64_t num_slots, int32_t cache_dtype, const kda_shape *s,
+                           kda_stream_t stream) {
+  kda_status st = check_cache(states, slots, cache, scales, num_slots, cache_dtype, s);
+  if (st != KDA_OK) return st;
+  return cuda_status(launch_state_cache(true, cache_dtype == KDA_CACHE_E4M3, s->head_dim_k,
+                                        s->head_dim_v, const_cast<float *>(states), slots, cache,
+                                        scales, s->num_seqs, s->num_heads, num_slots,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_state_load(const void *cache, const float *scales, const int32_t *slots,
+                          float *states, int64_t num_slots, int32_t cache_dtype,
+                          const kda_shape *s, kda_stream_t stream) {
+  kda_status st = check_cache(states, slots, cache, scales, num_slots, cache_dtype, s);
+  if (st != KDA_OK) return st;
+  return cuda_status(launch_state_cache(false, cache_dtype == KDA_CACHE_E4M3, s->head_dim_k,
+                                        s->head_dim_v, states, slots, const_cast<void *>(cache),
+                                        const_cast<float *>(scales), s->num_seqs, s->num_heads,
+                                        num_slots, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,178 @@
+// The 8-bit state cache: states quantised as they are written into slots, and
+// read back as FP32.
+//
+// Prefix caching keeps FP32 states of 4 D_k D_v bytes per head ("LLM -
+// Semianalysis, Kimi K3 아키텍처" (charstring.tistory.com/2557), Methods 3).  One
+// byte per element holds four times as many of them.  The decay is per key
+// channel, so the rows of a state differ in size by orders of magnitude: each
+// row (key channel) carries its own FP32 scale,
+//
+//   scale = max_v |S[c][v]| / top      (top = 448 for E4M3, 127 for INT8)
+//   code  = round(S[c][v] / scale)     (to nearest, ties to even; clamped to +-top)
+//   value = code * scale
+//
+// with both quotients correctly rounded, so the codes are reproducible to the
+// bit.  A row of zeros, or one so small that its scale underflows to zero,
+// stores zeros; a row that holds an infinity or a NaN stores a NaN scale and
+// reads back as NaN.
+//
+// Both kernels are bound by memory: 5/4 of the FP32 bytes cross HBM once.  One
+// CTA takes one (state, head), every thread's loads are issued before the first
+// use, and a row lies in one warp (D_v / 4 lanes of float4), so its maximum is a
+// shuffle reduction.
+#include <cuda_fp8.h>
+#include <math_constants.h>
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kCacheThreads = 256;
+
+template <bool E4M3> __device__ __forceinline__ float code_top() { return E4M3 ? 448.f : 127.f; }
+
+// Four codes of one row, packed in memory order.
+template <bool E4M3> __device__ __forceinline__ uint32_t encode4(float4 x, float scale) {
+  const float top = code_top<E4M3>();
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+  if (scale > 0.f) {   // false for a NaN scale too
+    y[0] = x.x / scale;
+    y[1] = x.y / scale;
+    y[2] = x.z / scale;
+    y[3] = x.w / scale;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fminf(fmaxf(y[i], -top), top);
+  }
+  if (E4M3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  }
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(y[i]) << (8 * i);
+  return r;
+}
+
+template <bool E4M3> __device__ __forceinline__ float4 decode4(uint32_t c, float scale) {
+  float4 x;
+  if (E4M3) {
+    const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
+    const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
+    const float2 a = __half22float2(lo), b = __half22float2(hi);
+    x = make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    x = make_float4((float)(int8_t)(c & 0xffu), (float)(int8_t)((c >> 8) & 0xffu),
+                    (float)(int8_t)((c >> 16) & 0xffu), (float)(int8_t)(c >> 24));
+  }
+  return make_float4(x.x * scale, x.y * scale, x.z * scale, x.w * scale);
+}
+
+template <int DK, int DV, bool E4M3>
+__global__ void __launch_bounds__(kCacheThreads)
+state_store_kernel(const float *__restrict__ states, const int32_t *__restrict__ slots,
+                   uint32_t *__restrict__ cache, float *__restrict__ scales, int N, int H,
+                   int64_t num_slots) {
+  constexpr int V4 = DV / 4;                          // lanes of one row
+  constexpr int RPP = kCacheThreads / V4;             // rows per pass
+  constexpr int ITER = DK / RPP;
+  static_assert(DK % RPP == 0 && ITER >= 1, "tile mismatch");
+  const int64_t unit = blockIdx.x;
+  const int n = (int)(unit / H), h = (int)(unit % H);
+  const int tid = threadIdx.x, cg = tid % V4, rg = tid / V4;
+  const int32_t slot = slots[n];
+  if (slot < 0 || (int64_t)slot >= num_slots) return;
+  const float4 *src = reinterpret_cast<const float4 *>(states) + unit * (DK * V4);
+  float4 x[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) x[i] = __ldcs(src + (rg + i * RPP) * V4 + cg);
+  // A slot named twice keeps the last entry's state, whichever CTA runs first.
+  int later = 0;
+  for (int j = n + 1 + tid; j < N; j += kCacheThreads) later |= slots[j] == slot;
+  if (__syncthreads_or(later)) return;
+  const int64_t dst_unit = (int64_t)slot * H + h;
+  uint32_t *dst = cache + dst_unit * (DK * V4);
+  float *sc = scales + dst_unit * DK;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int r = rg + i * RPP;
+    float m = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+    // fmaxf drops NaNs, and infinity * 0 is one: any of the two makes the scale NaN
+    float bad = x[i].x * 0.f + x[i].y * 0.f + x[i].z * 0.f + x[i].w * 0.f;
+#pragma unroll
+    for (int o = 1; o < V4; o <<= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      bad += __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    const float scale = bad == 0.f ? m / code_top<E4M3>() : CUDART_NAN_F;
+    dst[r * V4 + cg] = encode4<E4M3>(x[i], scale);
+    if (cg == 0) sc[r] = scale;
+  }
+}
+
+template <int DK, int DV, bool E4M3>
+__global__ void __launch_bounds__(kCacheThreads)
+state_load_kernel(const uint32_t *__restrict__ cache, const float *__restrict__ scales,
+                  const int32_t *__restrict__ slots, float *__restrict__ states, int H,
+                  int64_t num_slots) {
+  constexpr int V4 = DV / 4;
+  constexpr int RPP = kCacheThreads / V4;
+  constexpr int ITER = DK / RPP;
+  const int64_t unit = blockIdx.x;
+  const int n = (int)(unit / H), h = (int)(unit % H);
+  const int tid = threadIdx.x, cg = tid % V4, rg = tid / V4;
+  const int32_t slot = slots[n];
+  float4 *dst = reinterpret_cast<float4 *>(states) + unit * (DK * V4);
+  if (slot < 0 || (int64_t)slot >= num_slots) {   // no cached prefix: the zero state
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+      __stcs(dst + (rg + i * RPP) * V4 + cg, make_float4(0.f, 0.f, 0.f, 0.f));
+    return;
+  }
+  const int64_t src_unit = (int64_t)slot * H + h;
+  const uint32_t *src = cache + src_unit * (DK * V4);
+  const float *sc = scales + src_unit * DK;
+  uint32_t c[ITER];
+  float s[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) c[i] = __ldcs(src + (rg + i * RPP) * V4 + cg);
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) s[i] = sc[rg + i * RPP];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i)
+    __stcs(dst + (rg + i * RPP) * V4 + cg, decode4<E4M3>(c[i], s[i]));
+}
+
+template <int DK, int DV>
+cudaError_t launch_d(bool store, bool e4m3, float *states, const int32_t *slots, void *cache,
+                     float *scales, int N, int H, int64_t num_slots, cudaStream_t stream) {
+  const unsigned grid = (unsigned)((int64_t)N * H);
+  uint32_t *c = static_cast<uint32_t *>(cache);
+  if (store && e4m3)
+    state_store_kernel<DK, DV, true><<<grid, kCacheThreads, 0, stream>>>(states, slots, c, scales, N, H, num_slots);
+  else if (store)
+    state_store_kernel<DK, DV, false><<<grid, kCacheThreads, 0, stream>>>(states, slots, c, scales, N, H, num_slots);
+  else if (e4m3)
+    state_load_kernel<DK, DV, true><<<grid, kCacheThreads, 0, stream>>>(c, scales, slots, states, H, num_slots);
+  else
+    state_load_kernel<DK, DV, false><<<grid, kCacheThreads, 0, stream>>>(c, scales, slots, states, H, num_slots);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_state_cache(bool store, bool e4m3, int dk, int dv, float *states,
+                               const int32_t *slots, void *cache, float *scales, int N, int H,
+                               int64_t num_slots, cudaStream_t stream) {
+#define KDA_SC(DK_, DV_) \
+  if (dk == DK_ && dv == DV_) \
+    return launch_d<DK_, DV_>(store, e4m3, states, slots, cache, scales, N, H, num_slots, stream);
+  KDA_SC(32, 32) KDA_SC(32, 64) KDA_SC(32, 128)
+  KDA_SC(64, 32) KDA_SC(64, 64) KDA_SC(64, 128)
+  KDA_SC(128, 32) KDA_SC(128, 64) KDA_SC(128, 128)
+#undef KDA_SC
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kda

@@ -1,0 +1,328 @@
+// Verification of drafted tokens against the target's probabilities, from
+// given random numbers.
+//
+// For one sequence, context c is the committed prefix (-1) or a drafted token;
+// p_c and d_c are the target's and the draft's distributions after it.  With
+// r = p_c and R = 1, the successors of c are tried in the order of their places:
+//
+//   token x at place i is accepted when r(x) > 0 and u_i R d_c(x) < r(x)
+//   accepted: c = i, r = p_i, R = 1
+//   refused:  r = max(r / R - d_c, 0), R = sum(r)
+//
+// and when no successor is left the next token is the smallest j with
+// r(0) + ... + r(j) > u_last sum(r).  Accepted and drawn tokens then follow the
+// target's distribution exactly, for one drafted token per context (a chain)
+// and for several drawn from d_c (a tree).  Without a draft distribution (tokens
+// from a lookup, not a sample) d_c is one at the token itself: a refusal sets
+// r(x) = 0 and takes p_c(x) from R.
+//
+// Sums, quotients and comparisons are FP64: a token's border in the cumulative
+// sum has to come out the same whatever order the sum is taken in, and FP32
+// would move one draw in some hundreds at 10^5 tokens.
+//
+// Work: all successors' p and d are gathered at once, so a path of accepted
+// tokens reads no rows; only the last context's rows (and those of a context
+// with a refusal and a later successor) are read whole.  A cluster of 1 to 8
+// CTAs takes one sequence; its CTAs hold one slice of the vocabulary each, add
+// their sums over distributed shared memory, and the CTA whose slice holds the
+// border finds the token.  No atomics and no workspace: the result does not
+// depend on scheduling, and calls on any streams do not share anything.
+#include <cooperative_groups.h>
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kVThreads = 512;
+constexpr int kVWarps = kVThreads / 32;
+constexpr int kVMaxNodes = 64;
+constexpr int kVMaxCluster = 8;
+
+template <typename P> struct VecOf;
+template <> struct VecOf<float> { static constexpr int N = 4; };
+template <> struct VecOf<__nv_bfloat16> { static constexpr int N = 8; };
+
+template <typename P> __device__ __forceinline__ void unpack16(uint4 x, float *f);
+template <> __device__ __forceinline__ void unpack16<float>(uint4 x, float *f) {
+  f[0] = __uint_as_float(x.x); f[1] = __uint_as_float(x.y);
+  f[2] = __uint_as_float(x.z); f[3] = __uint_as_float(x.w);
+}
+template <> __device__ __forceinline__ void unpack16<__nv_bfloat16>(uint4 x, float *f) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// What is left of a context's target distribution after its refusals.
+struct Rest {
+  bool draft;             // refusals subtract the draft's row (else zero a token)
+  int m;                  // refusals so far
+  const double *inv;      // 1 / R before each of them
+  const int32_t *gone;    // the refused tokens
+  __device__ __forceinline__ double of(float p, float d, int token) const {
+    double r = (double)p;
+    if (draft) {
+      for (int l = 0; l < m; ++l) r = fmax(r * inv[l] - (double)d, 0.0);
+    } else {
+      for (int l = 0; l < m; ++l) r = gone[l] == token ? 0.0 : r;
+    }
+    return r;
+  }
+};
+
+// Sum of the rest over [lo, hi), over the calling lanes' strided elements.
+// A row starts where its element type aligns, no more: 16-byte loads when both
+// rows allow them, else single elements, several in flight.
+template <typename P>
+__device__ __forceinline__ double rest_sum(const P *p, const P *d, const Rest &rest, int lo,
+                                           int hi, int first, int stride) {
+  constexpr int V = VecOf<P>::N;
+  double acc = 0.0;
+  const bool sub = rest.draft && rest.m > 0;
+  if (((reinterpret_cast<uintptr_t>(p + lo) | (sub ? reinterpret_cast<uintptr_t>(d + lo) : 0)) & 15u) == 0) {
+    const int nv = (hi - lo) / V;
+    const uint4 *p4 = reinterpret_cast<const uint4 *>(p + lo);
+    const uint4 *d4 = reinterpret_cast<const uint4 *>(d + lo);
+#pragma unroll 4
+    for (int i = first; i < nv; i += stride) {
+      float a[V], b[V];
+      unpack16<P>(__ldg(p4 + i), a);
+      if (sub) unpack16<P>(__ldg(d4 + i), b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc += rest.of(a[e], sub ? b[e] : 0.f, lo + i * V + e);
+    }
+    for (int i = lo + nv * V + first; i < hi; i += stride)
+      acc += rest.of(to_f32(p[i]), sub ? to_f32(d[i]) : 0.f, i);
+  } else {
+#pragma unroll 8
+    for (int i = lo + first; i < hi; i += stride)
+      acc += rest.of(to_f32(p[i]), sub ? to_f32(d[i]) : 0.f, i);
+  }
+  return acc;
+}
+
+template <typename P>
+__global__ void __launch_bounds__(kVThreads)
+verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
+                   const int32_t *__restrict__ tokens, const int32_t *__restrict__ parents,
+                   const float *__restrict__ uniforms, int32_t *__restrict__ accept_node,
+                   int32_t *__restrict__ accept_len, int32_t *__restrict__ out_tokens, int T,
+                   int vocab) {
+  __shared__ int32_t s_tok[kVMaxNodes], s_par[kVMaxNodes], s_path[kVMaxNodes], s_gone[kVMaxNodes];
+  __shared__ float s_u[kVMaxNodes + 1];
+  __shared__ float s_p[kVMaxNodes], s_d[kVMaxNodes];
+  __shared__ double s_inv[kVMaxNodes];
+  __shared__ double s_warp[kVWarps], s_scan[kVWarps];
+  __shared__ double s_tot[2][kVMaxCluster];   // the CTAs' sums, one buffer per parity of the pass
+  __shared__ int s_last[kVWarps];
+
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.barrier_arrive();   // the others' shared memory exists once all have started
+  const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t n = blockIdx.x / CS;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const P *trow = target + n * (T + 1) * (int64_t)vocab;
+  const P *drow = draft ? draft + n * T * (int64_t)vocab : nullptr;
+
+  // Slices of whole 16-byte vectors: CTA, then warp.
+  constexpr int V = VecOf<P>::N;
+  const int piece = ((vocab + CS * kVWarps - 1) / (CS * kVWarps) + V - 1) / V * V;
+  const auto bound = [&](int w) {   // start of warp slice w of the whole cluster
+    const int64_t b = (int64_t)w * piece;
+    return (int)(b < vocab ? b : vocab);
+  };
+
+  if (tid <= T) s_u[tid] = uniforms[n * (T + 1) + tid];
+  if (tid < T) {
+    const int x = tokens[n * T + tid];
+    int up = parents ? parents[n * T + tid] : tid - 1;
+    if (up < -1 || up >= tid) up = -2;        // an empty place: never a successor
+    const bool in = x >= 0 && x < vocab;      // a token outside the vocabulary has no probability
+    s_tok[tid] = x;
+    s_par[tid] = up;
+    s_p[tid] = up >= -1 && in ? to_f32(trow[(int64_t)(up + 1) * vocab + x]) : 0.f;
+    s_d[tid] = drow && up >= -1 && in ? to_f32(drow[(int64_t)(up + 1) * vocab + x]) : 1.f;
+  }
+  __syncthreads();
+  cluster.barrier_wait();
+
+  // Every thread of the cluster takes the same decisions from here on.
+  Rest rest{drow != nullptr, 0, s_inv, s_gone};
+  int cur = -1, count = 0, pass = 0;
+  double R = 1.0;
+  // Sums of the rest over warps, CTAs and the cluster.
+  const auto sum_rest = [&] {
+    const int w = rank * kVWarps + warp;
+    double x = rest_sum<P>(trow + (int64_t)(cur + 1) * vocab,
+                           rest.draft ? drow + (int64_t)min(cur + 1, T - 1) * vocab : nullptr, rest,
+                           bound(w), bound(w + 1), lane, 32);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) s_warp[warp] = x;
+    __syncthreads();
+    const int buf = pass++ & 1;
+    if (tid < CS) {
+      double t = 0.0;
+#pragma unroll
+      for (int i = 0; i < kVWarps; ++i) t += s_warp[i];
+      cluster.map_shared_rank(&s_tot[buf][0], tid)[rank] = t;
+    }
+    cluster.sync();
+    double t = 0.0;
+    for (int i = 0; i < CS; ++i) t += s_tot[buf][i];
+    return t;
+  };
+
+  for (int i = 0; i < T; ++i) {
+    if (s_par[i] != cur) continue;
+    if (rest.draft && rest.m > 0) R = sum_rest();
+    const double r = rest.of(s_p[i], s_d[i], s_tok[i]);
+    if (r > 0.0 && (double)s_u[i] * R * (double)s_d[i] < r) {
+      if (tid == 0) s_path[count] = i;
+      ++count;
+      cur = i;
+      rest.m = 0;
+      R = 1.0;
+    } else {
+      __syncthreads();   // the rest's lists are read by every thread
+      if (tid == 0) {
+        s_inv[rest.m] = R > 0.0 ? 1.0 / R : 1.0;
+        s_gone[rest.m] = s_tok[i];
+      }
+      if (!rest.draft) R -= r;
+      ++rest.m;
+      __syncthreads();
+    }
+  }
+  double total = sum_rest();
+  if (!(total > 0.0) && rest.m > 0) {   // nothing is left: the target's own row
+    rest.m = 0;
+    total = sum_rest();
+  }
+  const int buf = (pass - 1) & 1;
+
+  if (rank == 0) {
+    if (tid == 0) {
+      accept_node[n] = cur;
+      accept_len[n] = count;
+    }
+    for (int i = tid; i <= T; i += kVThreads)
+      if (i != count) out_tokens[n * (T + 1) + i] = i < count ? s_tok[s_path[i]] : -1;
+  }
+
+  // The CTA, then the warp slice, that the border lies in: the first whose
+  // cumulative sum passes it, else (a random number of 1) the last with a part.
+  const double border = (double)s_u[T] * total;
+  int owner = -1, wown = 0;
+  double before = 0.0, run = 0.0;
+  bool found = false;
+  for (int i = 0; i < CS; ++i) {
+    const double t = s_tot[buf][i];
+    if (!found && t > 0.0) { owner = i; before = run; found = run + t > border; }
+    run += t;
+  }
+  if (owner < 0) {   // no token has a probability
+    if (rank == 0 && tid == 0) out_tokens[n * (T + 1) + count] = -1;
+    return;
+  }
+  if (owner != rank) return;
+  run = before;
+  found = false;
+  for (int i = 0; i < kVWarps; ++i) {
+    const double t = s_warp[i];
+    if (!found && t > 0.0) { wown = i; before = run; found = run + t > border; }
+    run += t;
+  }
+  // The warp slice over the whole CTA: a contiguous piece per thread, its sum,
+  // the threads' prefix sums, then the one piece that holds the border.
+  const int lo = bound(rank * kVWarps + wown), hi = bound(rank * kVWarps + wown + 1);
+  const int each = (hi - lo + kVThreads - 1) / kVThreads;
+  const int a = min(lo + tid * each, hi), b = min(a + each, hi);
+  const P *p = trow + (int64_t)(cur + 1) * vocab;
+  const P *d = rest.draft && rest.m > 0 ? drow + (int64_t)min(cur + 1, T - 1) * vocab : nullptr;
+  double mine = 0.0;
+  int last = -1;
+  for (int i = a; i < b; ++i) {
+    const double r = rest.of(to_f32(p[i]), d ? to_f32(d[i]) : 0.f, i);
+    mine += r;
+    if (r > 0.0) last = i;
+  }
+  double incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  int wlast = last;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wlast = max(wlast, __shfl_xor_sync(0xffffffffu, wlast, o));
+  if (lane == 31) s_scan[warp] = incl;
+  if (lane == 0) s_last[warp] = wlast;
+  __syncthreads();
+  double start = before;
+  int all_last = -1;
+  for (int i = 0; i < kVWarps; ++i) {
+    if (i < warp) start += s_scan[i];
+    all_last = max(all_last, s_last[i]);
+  }
+  // first token whose cumulative sum passes the border, or the slice's last
+  int hit = INT32_MAX;
+  double c = start + (incl - mine);
+  for (int i = a; i < b; ++i) {
+    const double r = rest.of(to_f32(p[i]), d ? to_f32(d[i]) : 0.f, i);
+    c += r;
+    if (r > 0.0 && c > border) { hit = i; break; }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) hit = min(hit, __shfl_xor_sync(0xffffffffu, hit, o));
+  __syncthreads();
+  if (lane == 0) s_last[warp] = hit;
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 0; i < kVWarps; ++i) hit = min(hit, s_last[i]);
+    out_tokens[n * (T + 1) + count] = hit == INT32_MAX ? all_last : hit;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_verify_tree(bool bf16, const void *target, const void *draft,
+                               const int32_t *tokens, const int32_t *parents,
+                               const float *uniforms, int32_t *accept_node, int32_t *accept_len,
+                               int32_t *out_tokens, int N, int T, int vocab, int num_sms,
+                               cudaStream_t stream) {
+  // CTAs per sequence: as many as keep the grid within four CTAs per SM (a
+  // lone sequence is bound by what its few SMs can load), at most the portable
+  // cluster size.
+  int cs = kVMaxCluster;
+  while (cs > 1 && (int64_t)N * cs > 4 * (int64_t)num_sms) cs >>= 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)N * cs));
+  cfg.blockDim = dim3(kVThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (bf16)
+    e = cudaLaunchKernelEx(&cfg, verify_tree_kernel<__nv_bfloat16>, (const __nv_bfloat16 *)target,
+                           (const __nv_bfloat16 *)draft, tokens, parents, uniforms, accept_node,
+                           accept_len, out_tokens, T, vocab);
+  else
+    e = cudaLaunchKernelEx(&cfg, verify_tree_kernel<float>, (const float *)target,
+                           (const float *)draft, tokens, parents, uniforms, accept_node,
+                           accept_len, out_tokens, T, vocab);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kda

@@ -16,13 +16,16 @@ LIB_PATH = os.path.join(_PKG, "libkda.so")
 
 KDA_OK, KDA_ERR_INVALID_ARGUMENT, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = range(5)
 KDA_DTYPE_F32, KDA_DTYPE_BF16 = 0, 1
+KDA_CACHE_E4M3, KDA_CACHE_INT8 = 0, 1
 
 EXPORTED = ("kda_prefill", "kda_prefill_ws", "kda_prefill_at", "kda_decode", "kda_decode_multi",
             "kda_ckpt_count", "kda_prefill_workspace_bytes", "kda_prefill_workspace_min_bytes",
             "kda_release_workspace_pool", "kda_prefill_path", "kda_selftest_bounded_wait",
             "kda_last_cuda_error", "kda_status_string", "kda_version", "kda_backward",
             "kda_backward_workspace_bytes", "kda_affine_rows", "kda_affine_state",
-            "kda_last_prefill_path", "kda_set_workspace_pool_cap", "kda_last_backward_path")
+            "kda_last_prefill_path", "kda_set_workspace_pool_cap", "kda_last_backward_path",
+            "kda_decode_tree", "kda_tree_commit", "kda_verify_tree", "kda_state_store",
+            "kda_state_load")
 
 # Largest workspace the binding allocates for the two-pass prefill; longer
 # inputs run in windows of chunks.
@@ -75,6 +78,16 @@ def load(path: str | None = None):
     lib.kda_decode.restype = ctypes.c_int
     lib.kda_decode_multi.argtypes = [P, P, P, P, P, P, P, P, I32, SP, P]
     lib.kda_decode_multi.restype = ctypes.c_int
+    lib.kda_decode_tree.argtypes = [P] * 8 + [I32, SP, P]
+    lib.kda_decode_tree.restype = ctypes.c_int
+    lib.kda_tree_commit.argtypes = [P] * 8 + [I32, SP, P]
+    lib.kda_tree_commit.restype = ctypes.c_int
+    lib.kda_verify_tree.argtypes = [P] * 8 + [I32, I32, I64, I32, P]
+    lib.kda_verify_tree.restype = ctypes.c_int
+    lib.kda_state_store.argtypes = [P, P, P, P, I64, I32, SP, P]
+    lib.kda_state_store.restype = ctypes.c_int
+    lib.kda_state_load.argtypes = [P, P, P, P, I64, I32, SP, P]
+    lib.kda_state_load.restype = ctypes.c_int
     lib.kda_ckpt_count.argtypes = [P, I32, I64]
     lib.kda_ckpt_count.restype = I64
     lib.kda_prefill_workspace_bytes.argtypes = [SP]
@@ -335,6 +348,148 @@ def kda_decode_multi(q, k, v, g, beta, state, *, accept_len=None, out=None, dev_
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_multi")
     return out
+
+
+def _want(name, t, shape, dtype, device):
+    """Check one argument of the calls below: a dense CUDA tensor of this shape and dtype."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be on one CUDA device with the other arguments, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _call(fn, device, stream, *args):
+    """Run a library call on the arguments' device and on ``stream`` (None: that
+    device's current stream)."""
+    with torch.cuda.device(device):
+        st = getattr(load(), fn)(*args, _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, fn)
+
+
+def _want_tree(k, v, g, beta, state, parents):
+    N, T, H, Dk = k.shape
+    Dv = v.shape[-1]
+    dev = k.device
+    _want("k", k, (N, T, H, Dk), k.dtype, dev)
+    _want("v", v, (N, T, H, Dv), k.dtype, dev)
+    _want("g", g, (N, T, H, Dk), torch.float32, dev)
+    _want("beta", beta, (N, T, H), torch.float32, dev)
+    _want("state", state, (N, H, Dk, Dv), torch.float32, dev)
+    if parents is not None:
+        _want("parents", parents, (N, T), torch.int32, dev)
+    return N, T, H, Dk, Dv
+
+
+def kda_decode_tree(q, k, v, g, beta, state, *, parents=None, out=None, stream=None):
+    """Outputs of a tree of drafted tokens over each sequence's state (see
+    kda_decode_tree in include/kda.h): q, k, g [N, T, H, Dk]; v [N, T, H, Dv];
+    beta [N, T, H]; state [N, H, Dk, Dv] FP32, only read; parents [N, T] int32
+    (place of the token before, -1 for the state, -2 for an empty place) or None
+    for chains; T <= 64.  Returns out [N, T, H, Dv], zero at empty places."""
+    N, T, H, Dk, Dv = _want_tree(k, v, g, beta, state, parents)
+    code = _dtype_code(k)
+    _want("q", q, k.shape, k.dtype, k.device)
+    if out is None:
+        out = torch.empty_like(v)
+    _want("out", out, v.shape, k.dtype, k.device)
+    shape = make_shape(N, N * T, H, Dk, Dv, 0, code)
+    _call("kda_decode_tree", k.device, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+          _ptr(state), _ptr(parents), _ptr(out), int(T), ctypes.byref(shape))
+    return out
+
+
+def kda_tree_commit(k, v, g, beta, state, accept_node, *, parents=None, state_out=None,
+                    stream=None):
+    """The state after place accept_node[n] (int32; outside [0, T) accepts
+    nothing) of each sequence's tree (see kda_tree_commit in include/kda.h),
+    written to ``state_out``, or over ``state`` when it is None.  Other
+    arguments as for kda_decode_tree.  Returns the tensor written."""
+    N, T, H, Dk, Dv = _want_tree(k, v, g, beta, state, parents)
+    code = _dtype_code(k)
+    _want("accept_node", accept_node, (N,), torch.int32, k.device)
+    if state_out is None:
+        state_out = state
+    _want("state_out", state_out, state.shape, torch.float32, k.device)
+    shape = make_shape(N, N * T, H, Dk, Dv, 0, code)
+    _call("kda_tree_commit", k.device, stream, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
+          _ptr(state_out), _ptr(parents), _ptr(accept_node), int(T), ctypes.byref(shape))
+    return state_out
+
+
+def kda_verify_tree(target_probs, tokens, uniforms, *, draft_probs=None, parents=None,
+                    accept_node=None, accept_len=None, out_tokens=None, stream=None):
+    """Verification of drafted tokens from given random numbers (see
+    kda_verify_tree in include/kda.h): target_probs [N, T + 1, V] and
+    draft_probs [N, T, V] (or None) FP32 or BF16; tokens and parents (or None
+    for chains) [N, T] int32; uniforms [N, T + 1] FP32 in [0, 1); T <= 64.
+    Returns (accept_node [N], accept_len [N], out_tokens [N, T + 1]), int32:
+    the last accepted place (-1: none), the number of accepted tokens (the
+    accept_len of kda_decode_multi), and the accepted tokens followed by the
+    one drawn and -1."""
+    N, T1, V = target_probs.shape
+    T, dev = T1 - 1, target_probs.device
+    code = _dtype_code(target_probs)
+    _want("target_probs", target_probs, (N, T1, V), target_probs.dtype, dev)
+    if draft_probs is not None:
+        _want("draft_probs", draft_probs, (N, T, V), target_probs.dtype, dev)
+    _want("tokens", tokens, (N, T), torch.int32, dev)
+    if parents is not None:
+        _want("parents", parents, (N, T), torch.int32, dev)
+    _want("uniforms", uniforms, (N, T1), torch.float32, dev)
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
+    accept_node = new(N) if accept_node is None else accept_node
+    accept_len = new(N) if accept_len is None else accept_len
+    out_tokens = new(N, T1) if out_tokens is None else out_tokens
+    _want("accept_node", accept_node, (N,), torch.int32, dev)
+    _want("accept_len", accept_len, (N,), torch.int32, dev)
+    _want("out_tokens", out_tokens, (N, T1), torch.int32, dev)
+    _call("kda_verify_tree", dev, stream, _ptr(target_probs), _ptr(draft_probs), _ptr(tokens),
+          _ptr(parents), _ptr(uniforms), _ptr(accept_node), _ptr(accept_len), _ptr(out_tokens),
+          int(N), int(T), int(V), code)
+    return accept_node, accept_len, out_tokens
+
+
+def _want_cache(states, slots, cache, scales):
+    n, H, Dk, Dv = states.shape
+    dev = states.device
+    codes = {torch.float8_e4m3fn: KDA_CACHE_E4M3, torch.int8: KDA_CACHE_INT8}
+    if cache.dtype not in codes:
+        raise TypeError(f"cache must be float8_e4m3fn or int8, got {cache.dtype}")
+    num_slots = cache.shape[0]
+    _want("states", states, (n, H, Dk, Dv), torch.float32, dev)
+    _want("slots", slots, (n,), torch.int32, dev)
+    _want("cache", cache, (num_slots, H, Dk, Dv), cache.dtype, dev)
+    _want("scales", scales, (num_slots, H, Dk), torch.float32, dev)
+    return int(num_slots), codes[cache.dtype], make_shape(n, n, H, Dk, Dv, 0, KDA_DTYPE_F32)
+
+
+def kda_state_store(states, slots, cache, scales, *, stream=None):
+    """Quantise states [n, H, Dk, Dv] (FP32) into the slots slots[n] (int32;
+    outside the cache: skipped; named twice: the last stays) of the state cache
+    (see kda_state_store in include/kda.h): cache [num_slots, H, Dk, Dv]
+    (float8_e4m3fn or int8), scales [num_slots, H, Dk] FP32.  Returns (cache,
+    scales)."""
+    num_slots, code, shape = _want_cache(states, slots, cache, scales)
+    _call("kda_state_store", states.device, stream, _ptr(states), _ptr(slots), _ptr(cache),
+          _ptr(scales), num_slots, code, ctypes.byref(shape))
+    return cache, scales
+
+
+def kda_state_load(cache, scales, slots, *, states=None, stream=None):
+    """Read the states of the slots slots[n] (outside the cache: the zero state)
+    back from the state cache.  Returns states [n, H, Dk, Dv] FP32."""
+    if states is None:
+        states = torch.empty(slots.numel(), *cache.shape[1:], dtype=torch.float32,
+                             device=cache.device)
+    num_slots, code, shape = _want_cache(states, slots, cache, scales)
+    _call("kda_state_load", states.device, stream, _ptr(cache), _ptr(scales), _ptr(slots),
+          _ptr(states), num_slots, code, ctypes.byref(shape))
+    return states
 
 
 def kda_selftest_bounded_wait(dev_status, max_polls: int, stream=None) -> None:
