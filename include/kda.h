@@ -327,8 +327,9 @@ kda_status kda_verify_tree(const void *target_probs, const void *draft_probs,
 /*
  * The 8-bit state cache: a pool of num_slots states for prefix caching, a
  * quarter of the FP32 size.  Each row (key channel) of a state has one FP32
- * scale, its largest magnitude over the code type's largest value (448 for E4M3,
- * 127 for INT8); a code is the element over the scale, rounded to nearest even.
+ * scale, its largest magnitude times 1 / top in FP32 (top: the code type's largest
+ * value, 448 for E4M3, 127 for INT8); a code is the element over the scale, rounded
+ * to nearest even and clamped to +-top.
  * Rows of zeros store zeros; a row that holds an infinity or a NaN reads back as
  * NaN.
  *

@@ -38,7 +38,6 @@
 namespace kda {
 namespace {
 
-constexpr int kMaxNodes = 64;
 constexpr float kGamLimit = 80.f;
 constexpr float kFactorLimit = 1e36f;
 
@@ -48,13 +47,21 @@ __device__ __forceinline__ uint32_t tf32_rn(float x) {
   return r;
 }
 
-// One operand value: rounded to TF32, and for X3 what the rounding left.
+// An operand of the products.  For X3 it is an FP32 value, split into two TF32
+// terms where it is used; otherwise it is a value rounded to TF32 when it was made
+// (operand<X3>), whose bits go in as they are.
+template <bool X3> __device__ __forceinline__ float operand(float x) {
+  return X3 ? x : __uint_as_float(tf32_rn(x));
+}
 template <bool X3> struct Op {
   uint32_t hi, lo;
-  __device__ __forceinline__ Op() {}
   __device__ __forceinline__ explicit Op(float x) {
-    hi = tf32_rn(x);
-    if (X3) lo = tf32_rn(x - __uint_as_float(hi));
+    if (X3) {
+      hi = tf32_rn(x);
+      lo = tf32_rn(x - __uint_as_float(hi));
+    } else {
+      hi = __float_as_uint(x);
+    }
   }
 };
 
@@ -77,9 +84,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const Op<X3> &a0, const Op<X3
   mma_raw(c, a0.hi, a1.hi, a2.hi, a3.hi, b0.hi, b1.hi);
 }
 
-// Position of key channel c in a token row: the four channels 4 m + j (m = 0..3)
-// of a group of 16 that lane j of a quad needs lie side by side.
-__device__ __forceinline__ int spot(int c) { return (c & ~15) | ((c & 3) << 2) | ((c >> 2) & 3); }
+// Token rows lie in shared memory without padding, in 16-byte units whose low
+// three index bits are exclusive-ored with this function of the row: reads of
+// units 4 a + j of rows 8 i + gid, and writes of unit gid (or half a unit) of rows
+// 8 i + 2 j + e, touch distinct banks.
+__device__ __forceinline__ int swizzle(int row) { return ((row & 6) ^ ((row & 1) << 2)); }
 
 // E consecutive elements as floats (2 or 4).
 template <int E> __device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float *x) {
@@ -121,22 +130,25 @@ template <int E> __device__ __forceinline__ void store_row(float *p, const float
   else *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
 }
 
+// Sets of places: 32 bits do for up to four tiles.
+template <int NT> struct MaskOf { using T = uint32_t; };
+template <> struct MaskOf<8> { using T = unsigned long long; };
+
 // NT: tiles of 8 places (places past T are empty ones).
 template <int DK, int DV, int NT, typename TIn> struct TreeCfg {
   static constexpr bool X3 = sizeof(TIn) == 4;
   static constexpr int MT = NT == 8 || X3 ? 1 : 2;  // 16-column tiles per warp (registers)
-  static constexpr int E = 2 * MT;                  // value columns per lane
+  static constexpr int E = 2 * MT;                  // value columns, or key channels, per lane
   static constexpr int WARPS = DV / (16 * MT);
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int T8 = 8 * NT;
   static constexpr int NB = NT < 2 ? 1 : NT / 2;    // diagonal blocks
   static constexpr int BT = NT < 2 ? 1 : 2;         // tiles per diagonal block
-  static constexpr int LDK = DK + 16;               // 16-byte reads of 8 rows: distinct banks
-  static constexpr int LDT = T8 + (T8 == 8 ? 0 : 8);   // = 8 or 24 modulo 32: 8-byte reads
+  static constexpr int LDT = T8 + (T8 == 8 ? 0 : 8);   // = 8 or 24 modulo 32: 8-byte accesses
   static constexpr int LDB = 8 * BT + (BT == 1 ? 0 : 8);
   // shared memory, in floats
-  static constexpr int KT = 0, QT = KT + T8 * LDK, KH = QT + T8 * LDK;
-  static constexpr int LM = KH + T8 * LDK, PM = LM + T8 * LDT;
+  static constexpr int KT = 0, QT = KT + T8 * DK, KH = QT + T8 * DK;
+  static constexpr int LM = KH + T8 * DK, PM = LM + T8 * LDT;
   static constexpr int MI = PM + T8 * LDT;          // (I + L)^-1 of the diagonal blocks
   static constexpr int BE = MI + NB * 8 * BT * LDB;
   static constexpr int TOTAL = BE + T8;
@@ -150,14 +162,15 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
                    const float *__restrict__ beta, const float *__restrict__ state,
                    const int32_t *__restrict__ parents, TIn *__restrict__ out, int T, int H) {
   using Cfg = TreeCfg<DK, DV, NT, TIn>;
+  using Mask = typename MaskOf<NT>::T;
   constexpr bool X3 = Cfg::X3;
-  constexpr int MT = Cfg::MT, E = Cfg::E, T8 = Cfg::T8, LDK = Cfg::LDK, LDT = Cfg::LDT;
-  constexpr int LDB = Cfg::LDB, BT = Cfg::BT, NB = Cfg::NB, THREADS = Cfg::THREADS;
+  constexpr int MT = Cfg::MT, E = Cfg::E, T8 = Cfg::T8, LDT = Cfg::LDT;
+  constexpr int LDB = Cfg::LDB, BT = Cfg::BT, NB = Cfg::NB;
   extern __shared__ __align__(16) float sm[];
   float *s_kt = sm + Cfg::KT, *s_qt = sm + Cfg::QT, *s_kh = sm + Cfg::KH;
   float *s_L = sm + Cfg::LM, *s_P = sm + Cfg::PM, *s_M = sm + Cfg::MI, *s_beta = sm + Cfg::BE;
-  __shared__ unsigned long long s_anc[kMaxNodes];   // ancestors and self; 0: an empty place
-  __shared__ int s_par[kMaxNodes], s_jump[kMaxNodes];
+  __shared__ Mask s_anc[T8];           // ancestors and self; 0: an empty place
+  __shared__ int s_par[T8], s_jump[T8], s_tiles;
 
   const int64_t unit = blockIdx.x;
   const int n = (int)(unit / H), h = (int)(unit % H);
@@ -165,162 +178,259 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   const int gid = lane >> 2, j = lane & 3;
   const int64_t row0 = (int64_t)n * T * H + h;      // token t is row row0 + t H
 
-  // ---- the state's columns of this warp: rows 4 m + j, columns col .. col + E - 1 ----
+  int up[T8 > 32 ? 2 : 1];             // predecessors of places lane (and lane + 32)
+  if (warp == 0) {
+#pragma unroll
+    for (int e = 0; e < (T8 > 32 ? 2 : 1); ++e) {
+      const int t = lane + 32 * e;
+      up[e] = -2;
+      if (t < T) up[e] = parents ? __ldg(parents + (int64_t)n * T + t) : t - 1;
+    }
+  }
+
+  // ---- the state's columns of this warp: rows 16 a + 4 j + m, columns col .. col + E - 1 ----
   const int col = 16 * MT * warp + E * gid;
   float s0[DK / 4][E];
   {
-    const float *src = state + unit * (DK * DV) + (int64_t)j * DV + col;
+    const float *src = state + unit * (DK * DV) + (int64_t)(4 * j) * DV + col;
 #pragma unroll
     for (int m = 0; m < DK / 4; ++m) {
+      const float *at = src + ((m >> 2) * 16 + (m & 3)) * DV;
       if (E == 4)
         asm volatile("ld.global.cs.v4.f32 {%0,%1,%2,%3}, [%4];"
                      : "=f"(s0[m][0]), "=f"(s0[m][1]), "=f"(s0[m][E - 2]), "=f"(s0[m][E - 1])
-                     : "l"(src + m * 4 * DV));
+                     : "l"(at));
       else
         asm volatile("ld.global.cs.v2.f32 {%0,%1}, [%2];"
                      : "=f"(s0[m][0]), "=f"(s0[m][1])
-                     : "l"(src + m * 4 * DV));
+                     : "l"(at));
     }
   }
 
-  // ---- ancestors by pointer doubling (one warp) ----
+  // ---- ancestors by pointer doubling (one warp): after the step of size d every
+  //      mask holds the last 2 d places of its path ----
   if (warp == 0) {
-    for (int t = lane; t < kMaxNodes; t += 32) {
-      int up = -2;
-      if (t < T) up = parents ? parents[(int64_t)n * T + t] : t - 1;
-      if (up < -1 || up >= t) up = -2;
-      s_par[t] = up;
-      s_jump[t] = up;
-      s_anc[t] = 1ull << t;
+    if (T8 <= 32) {
+      if (up[0] < -1 || up[0] >= lane) up[0] = -2;
+      int jump = up[0];
+      uint32_t m = 1u << lane;
+      for (int d = 1; d < T; d <<= 1) {
+        const uint32_t mo = __shfl_sync(0xffffffffu, m, jump & 31);
+        const int jo = __shfl_sync(0xffffffffu, jump, jump & 31);
+        if (jump >= 0) { m |= mo; jump = jo; }
+      }
+      if (jump != -1) m = 0;                           // a path that ends in an empty place
+      if (lane < T8) { s_anc[lane] = (Mask)m; s_par[lane] = up[0]; }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = lane + 32 * e;
+        int &u = up[T8 > 32 ? e : 0];
+        if (u < -1 || u >= t) u = -2;
+        if (t < T8) {
+          s_par[t] = u;
+          s_jump[t] = u;
+          s_anc[t] = (Mask)1 << (t < T8 ? t : 0);
+        }
+      }
+      __syncwarp();
+      for (int d = 1; d < T; d <<= 1) {
+        Mask m[2];
+        int jo[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = (lane + 32 * e) % T8, a = s_jump[t];
+          m[e] = s_anc[t] | (a >= 0 ? s_anc[a] : (Mask)0);
+          jo[e] = a >= 0 ? s_jump[a] : a;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s_anc[(lane + 32 * e) % T8] = m[e];
+          s_jump[(lane + 32 * e) % T8] = jo[e];
+        }
+        __syncwarp();
+      }
+      for (int t = lane; t < T8; t += 32)
+        if (s_jump[t] != -1) s_anc[t] = 0;
     }
     __syncwarp();
-    // after the step of size d every mask holds the last 2 d places of its path
-    for (int d = 1; d < T; d <<= 1) {
-      unsigned long long m[2];
-      int up[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = lane + 32 * e, a = s_jump[t];
-        m[e] = s_anc[t] | (a >= 0 ? s_anc[a] : 0ull);
-        up[e] = a >= 0 ? s_jump[a] : a;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s_anc[lane + 32 * e] = m[e];
-        s_jump[lane + 32 * e] = up[e];
-      }
-      __syncwarp();
+    // tiles up to the last token that is there; the rest is not computed
+    int last = -1;
+    for (int t = lane; t < T8; t += 32) {
+      const bool live = s_anc[t] != 0;
+      s_beta[t] = live ? beta[row0 + (int64_t)t * H] : 0.f;
+      if (live) last = t;
     }
-    for (int t = lane; t < kMaxNodes; t += 32)      // a path that ends in an empty place
-      if (s_jump[t] != -1) s_anc[t] = 0;
-    for (int t = lane; t < T8; t += 32)
-      s_beta[t] = t < T && s_anc[t] != 0 ? beta[row0 + (int64_t)t * H] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+    if (lane == 0) s_tiles = (last + 8) >> 3;
   }
   __syncthreads();
+  const int tiles = s_tiles;
 
-  // ---- Gam along the paths; Kt, Qt, Kh ----
+  // ---- Gam along the paths, Kt, Qt, Kh.  Gam^T = g^T A^T with A the 0/1 matrix of
+  //      ancestors, a product as well: a lane brings g, and gets Gam, of places
+  //      8 i + 2 j, + 1 in E channels.  g goes in as two TF32 terms (2^-23 of it is
+  //      lost); for X3 as multiples of 1/8, whose sums are exact, and two terms for
+  //      the rest, with sums of their own. ----
   bool wide = false;   // factors out of range: L and P pair by pair
-  for (int c = tid; c < DK; c += THREADS) {
-    const int p = spot(c);
-    constexpr int U = 8;
-    float gam = 0.f, low = 0.f;          // of the place before, kept for chains
-    for (int t0 = 0; t0 < T8; t0 += U) {
-      float gv[U], kv[U], qv[U];
+  for (int cw = warp; cw < DK / (16 * MT); cw += Cfg::WARPS) {
+    const int c0 = 16 * MT * cw + E * gid;
+    float gam[NT][MT][4], low[X3 ? NT : 1][MT][4];
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int t = t0 + i;
-        gv[i] = kv[i] = qv[i] = 0.f;
-        if (t < T) {
-          const int64_t at = (row0 + (int64_t)t * H) * DK + c;
-          gv[i] = __ldg(g + at);
-          kv[i] = to_f32(k[at]);
-          qv[i] = to_f32(q[at]);
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gam[i][m][e] = 0.f;
+          if (X3) low[X3 ? i : 0][m][e] = 0.f;
         }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i >= tiles) break;
+      float x[2][E];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = 8 * i + 2 * j + e;
+#pragma unroll
+        for (int c = 0; c < E; ++c) x[e][c] = 0.f;
+        if (s_anc[t] != 0) load_row<E>(g + (row0 + (int64_t)t * H) * DK + c0, x[e]);
       }
+      uint32_t hi[MT][4], lo[MT][4], lo2[MT][4];
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int t = t0 + i, up = s_par[t];
-        const bool live = s_anc[t] != 0;
-        float b = 0.f, bl = 0.f;
-        if (up == t - 1 && t > 0) {
-          b = gam;
-          bl = low;
-        } else if (up >= 0) {
-          // until every place has been reached, Kh's rows hold Gam (and Qt's its low part)
-          b = s_kh[up * LDK + p];
-          if (X3) bl = s_qt[up * LDK + p];
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y = x[e >> 1][2 * m + (e & 1)];   // a0, a1: place 2 j; a2, a3: place 2 j + 1
+          if (X3) {
+            y = fmaxf(y, -128.f);                 // exp(-128) is 0 in FP32 already
+            const float r = rintf(y * 8.f) * 0.125f;
+            hi[m][e] = __float_as_uint(r);
+            y -= r;
+            lo[m][e] = tf32_rn(y);
+            lo2[m][e] = tf32_rn(y - __uint_as_float(lo[m][e]));
+          } else {
+            hi[m][e] = tf32_rn(y);
+            lo[m][e] = tf32_rn(y - __uint_as_float(hi[m][e]));
+          }
         }
-        const float gt = live ? gv[i] : 0.f;
-        gam = b + gt;
-        if (X3) {   // two-sum: the rounding of b + g_t
-          const float z = gam - b;
-          low = bl + ((b - (gam - z)) + (gt - z));
+#pragma unroll
+      for (int r = i; r < NT; ++r) {
+        const uint32_t bits = (uint32_t)(s_anc[8 * r + gid] >> (8 * i + 2 * j));
+        const uint32_t b0 = bits & 1 ? 0x3f800000u : 0u, b1 = bits & 2 ? 0x3f800000u : 0u;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma_raw(gam[r][m], hi[m][0], hi[m][1], hi[m][2], hi[m][3], b0, b1);
+          mma_raw(X3 ? low[X3 ? r : 0][m] : gam[r][m], lo[m][0], lo[m][1], lo[m][2], lo[m][3], b0, b1);
+          if (X3) mma_raw(low[X3 ? r : 0][m], lo2[m][0], lo2[m][1], lo2[m][2], lo2[m][3], b0, b1);
         }
-        s_kh[t * LDK + p] = gam;
-        if (X3) s_qt[t * LDK + p] = low;
-        s_kt[t * LDK + p] = live ? kv[i] : 0.f;
-        if (!X3) s_qt[t * LDK + p] = live ? qv[i] : 0.f;
       }
     }
-    for (int t = 0; t < T8; ++t) {
-      const float G = s_kh[t * LDK + p], kc = s_kt[t * LDK + p];
-      float down, up, qc;
-      if (X3) {
-        const float lo = s_qt[t * LDK + p];
-        qc = t < T && s_anc[t] != 0 ? to_f32(q[(row0 + (int64_t)t * H) * DK + c]) : 0.f;
-        down = expf(G);
-        down += down * lo;
-        up = expf(-G);
-        up -= up * lo;
-      } else {
-        qc = s_qt[t * LDK + p];
-        down = __expf(G);
-        up = __expf(-G);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i >= tiles) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = 8 * i + 2 * j + e;
+        float kv[E], qv[E], kh[E];
+#pragma unroll
+        for (int c = 0; c < E; ++c) kv[c] = qv[c] = 0.f;
+        if (s_anc[t] != 0) {
+          const int64_t at = (row0 + (int64_t)t * H) * DK + c0;
+          load_row<E>(k + at, kv);
+          load_row<E>(q + at, qv);
+        }
+#pragma unroll
+        for (int c = 0; c < E; ++c) {
+          float G = gam[i][c >> 1][2 * (c & 1) + e], down, inv;
+          if (X3) {
+            const float b = low[X3 ? i : 0][c >> 1][2 * (c & 1) + e];
+            const float sum = G + b, rest = b - (sum - G);
+            G = sum;
+            down = expf(G);
+            down += down * rest;
+            inv = expf(-G);
+            inv -= inv * rest;
+          } else {
+            down = __expf(G);
+            inv = __expf(-G);
+          }
+          kh[c] = operand<X3>(kv[c] * inv);
+          kv[c] = operand<X3>(kv[c] * down);
+          qv[c] = operand<X3>(qv[c] * down);
+          wide |= !(fabsf(kh[c]) < kFactorLimit) || !(fabsf(G) <= kGamLimit);
+        }
+        const int at = t * DK + ((((c0 >> 2) ^ swizzle(t)) << 2) | (c0 & 3));
+        store_row<E>(s_kt + at, kv);
+        store_row<E>(s_qt + at, qv);
+        store_row<E>(s_kh + at, kh);
       }
-      const float kt = kc * down, qt = qc * down, kh = kc * up;
-      wide |= !(fabsf(kh) < kFactorLimit) || !(fabsf(G) <= kGamLimit);
-      s_kt[t * LDK + p] = X3 ? kt : __uint_as_float(tf32_rn(kt));
-      s_qt[t * LDK + p] = X3 ? qt : __uint_as_float(tf32_rn(qt));
-      s_kh[t * LDK + p] = X3 ? kh : __uint_as_float(tf32_rn(kh));
     }
+  }
+
+  // ---- -V, transposed: what the products below are added to (columns x places) ----
+  float vn[NT][MT][4];
+  {
+    const TIn *vp = v + row0 * DV + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = 8 * i + 2 * j + e;
+        float x[E];
+#pragma unroll
+        for (int c = 0; c < E; ++c) x[c] = 0.f;
+        if (s_anc[t] != 0) load_row<E>(vp + (int64_t)t * H * DV, x);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          vn[i][m][e] = -x[2 * m];
+          vn[i][m][2 + e] = -x[2 * m + 1];
+        }
+      }
   }
   wide = __syncthreads_or(wide);
 
+  // Where this lane's 16-byte units of channels 16 a + 4 j lie in a row 8 i + gid.
+  const int even = gid * DK + ((j ^ swizzle(gid)) << 2), odd = even ^ 16;
+  const auto unit_at = [&](const float *rows, int i, int a) {
+    return *reinterpret_cast<const float4 *>(rows + 8 * i * DK + 32 * (a >> 1) + (a & 1 ? odd : even));
+  };
+  // L as the diagonal blocks' inverses need it, -L as an operand elsewhere.
+  const auto put = [&](int t, int s, float lt, float pt) {
+    s_L[t * LDT + s] = t / (8 * BT) == s / (8 * BT) ? lt : operand<X3>(-lt);
+    s_P[t * LDT + s] = operand<X3>(pt);
+  };
+
   // ---- L and P: tile (a, b) of 8 x 8 places, rows Kt and Qt of one tile in one product ----
   if (!wide) {
-    for (int tile = warp; tile < NT * (NT + 1) / 2; tile += Cfg::WARPS) {
+    for (int tile = warp; tile < tiles * (tiles + 1) / 2; tile += Cfg::WARPS) {
       int a = 0;
       while ((a + 1) * (a + 2) / 2 <= tile) ++a;
       const int b = tile - a * (a + 1) / 2;
       float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
-      const float *pk = s_kt + (8 * a + gid) * LDK + 4 * j;
-      const float *pq = s_qt + (8 * a + gid) * LDK + 4 * j;
-      const float *ph = s_kh + (8 * b + gid) * LDK + 4 * j;
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(pk + 16 * i);
-        const float4 y = *reinterpret_cast<const float4 *>(pq + 16 * i);
-        const float4 z = *reinterpret_cast<const float4 *>(ph + 16 * i);
+        const float4 x = unit_at(s_kt, a, i), y = unit_at(s_qt, a, i), z = unit_at(s_kh, b, i);
         mma<X3>(c, Op<X3>(x.x), Op<X3>(y.x), Op<X3>(x.y), Op<X3>(y.y), Op<X3>(z.x), Op<X3>(z.y));
         mma<X3>(c2, Op<X3>(x.z), Op<X3>(y.z), Op<X3>(x.w), Op<X3>(y.w), Op<X3>(z.z), Op<X3>(z.w));
       }
       const int t = 8 * a + gid;
-      const unsigned long long anc = s_anc[t];
+      const Mask anc = s_anc[t];
       const float bt = s_beta[t];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int s = 8 * b + 2 * j + e;
         const bool on = (anc >> s) & 1;
-        s_L[t * LDT + s] = on && s != t ? bt * (c[e] + c2[e]) : 0.f;
-        s_P[t * LDT + s] = on ? c[2 + e] + c2[2 + e] : 0.f;
+        put(t, s, on && s != t ? bt * (c[e] + c2[e]) : 0.f, on ? c[2 + e] + c2[2 + e] : 0.f);
       }
     }
   } else {
     // One warp per place: the path upwards, with the decay between its ends summed
     // from the near one, so that no large sums are subtracted.
-    for (int t = warp; t < T8; t += Cfg::WARPS) {
-      for (int s = lane; s <= (t | 7); s += 32) s_L[t * LDT + s] = s_P[t * LDT + s] = 0.f;
+    for (int t = warp; t < 8 * tiles; t += Cfg::WARPS) {
+      for (int s = lane; s <= (t | 7); s += 32) put(t, s, 0.f, 0.f);
       __syncwarp();
       const int64_t rt = (row0 + (int64_t)t * H) * DK + lane;
       float kt[DK / 32], qt[DK / 32], d[DK / 32];
@@ -346,83 +456,81 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
           kk += __shfl_xor_sync(0xffffffffu, kk, o);
           qk += __shfl_xor_sync(0xffffffffu, qk, o);
         }
-        if (lane == 0) {
-          s_L[t * LDT + s] = s != t ? s_beta[t] * kk : 0.f;
-          s_P[t * LDT + s] = qk;
-        }
+        if (lane == 0) put(t, s, s != t ? s_beta[t] * kk : 0.f, qk);
       }
     }
   }
   __syncthreads();
 
-  // ---- inverses of the diagonal blocks of I + L: lane = column, forward substitution ----
-  for (int b = warp; b < NB; b += Cfg::WARPS) {
+  // ---- M = (I + L)^-1 of the diagonal blocks, a lane per row, from M (I + L) = I:
+  //      once entry s is final, row s of L takes it out of the entries before ----
+  if (warp < (NB + 1) / 2) {
     constexpr int B = 8 * BT;
+    const int b = min(2 * warp + (lane >> 4), NB - 1), r = lane & 15;
     const float *L = s_L + b * B * LDT + b * B;
     float x[B];
 #pragma unroll
-    for (int t = 0; t < B; ++t) {
-      float y0 = t == lane ? 1.f : 0.f, y1 = 0.f;
+    for (int s = 0; s < B; ++s) x[s] = s == r ? 1.f : 0.f;
+    if (B * b < 8 * tiles) {
 #pragma unroll
-      for (int s = 0; s < t; ++s) {
-        if (s & 1) y1 -= L[t * LDT + s] * x[s];
-        else y0 -= L[t * LDT + s] * x[s];
+      for (int s = B - 1; s > 0; --s) {
+        if (BT == 2 && s >= 8 && 8 * (2 * b + 1) >= 8 * tiles) continue;   // rows not computed
+#pragma unroll
+        for (int e = 0; e < s; e += 4) {
+          const float4 l = *reinterpret_cast<const float4 *>(L + s * LDT + e);
+          x[e] -= x[s] * l.x;
+          if (e + 1 < s) x[e + 1] -= x[s] * l.y;
+          if (e + 2 < s) x[e + 2] -= x[s] * l.z;
+          if (e + 3 < s) x[e + 3] -= x[s] * l.w;
+        }
       }
-      x[t] = y0 + y1;
     }
-    if (lane < B)
+    if (r < B && (lane < 16 || NB > 1))
 #pragma unroll
-      for (int t = 0; t < B; ++t) s_M[(b * B + t) * LDB + lane] = x[t];
+      for (int s = 0; s < B; s += 4)
+        *reinterpret_cast<float4 *>(s_M + (b * B + r) * LDB + s) =
+            make_float4(operand<X3>(x[s]), operand<X3>(x[s + 1]), operand<X3>(x[s + 2]),
+                        operand<X3>(x[s + 3]));
   }
 
-  // ---- Kt S0 - V, transposed: accumulators hold columns x places ----
-  const TIn *vp = v + row0 * DV + col;
-  float vn[NT][MT][4];
+  // ---- Kt S0 - V and Qt S0, transposed, in one pass over the state ----
+  float o[NT][MT][4];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int t = 8 * i + 2 * j + e;
-      float x[E];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int c = 0; c < E; ++c) x[c] = 0.f;
-      if (t < T && s_anc[t] != 0) load_row<E>(vp + (int64_t)t * H * DV, x);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        vn[i][m][e] = -x[2 * m];
-        vn[i][m][2 + e] = -x[2 * m + 1];
-      }
-    }
-  }
+      for (int e = 0; e < 4; ++e) o[i][m][e] = 0.f;
 #pragma unroll
   for (int a = 0; a < DK / 16; ++a) {
-    Op<X3> A[2][MT][4];   // the two k8 tiles of these 16 state rows
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        A[w][m][0] = Op<X3>(s0[4 * a + 2 * w][2 * m]);
-        A[w][m][1] = Op<X3>(s0[4 * a + 2 * w][2 * m + 1]);
-        A[w][m][2] = Op<X3>(s0[4 * a + 2 * w + 1][2 * m]);
-        A[w][m][3] = Op<X3>(s0[4 * a + 2 * w + 1][2 * m + 1]);
-      }
+      for (int e = 0; e < E; ++e) s0[4 * a + m][e] = operand<X3>(s0[4 * a + m][e]);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const float4 x = *reinterpret_cast<const float4 *>(s_kt + (8 * i + gid) * LDK + 16 * a + 4 * j);
-      const Op<X3> b0(x.x), b1(x.y), b2(x.z), b3(x.w);
+      if (i >= tiles) break;
+      const float4 x = unit_at(s_kt, i, a), y = unit_at(s_qt, i, a);
+      const Op<X3> x0(x.x), x1(x.y), x2(x.z), x3(x.w), y0(y.x), y1(y.y), y2(y.z), y3(y.w);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        mma<X3>(vn[i][m], A[0][m][0], A[0][m][1], A[0][m][2], A[0][m][3], b0, b1);
-        mma<X3>(vn[i][m], A[1][m][0], A[1][m][1], A[1][m][2], A[1][m][3], b2, b3);
+        const Op<X3> a0(s0[4 * a][2 * m]), a1(s0[4 * a][2 * m + 1]), a2(s0[4 * a + 1][2 * m]),
+            a3(s0[4 * a + 1][2 * m + 1]);
+        mma<X3>(vn[i][m], a0, a1, a2, a3, x0, x1);
+        mma<X3>(o[i][m], a0, a1, a2, a3, y0, y1);
+        const Op<X3> d0(s0[4 * a + 2][2 * m]), d1(s0[4 * a + 2][2 * m + 1]),
+            d2(s0[4 * a + 3][2 * m]), d3(s0[4 * a + 3][2 * m + 1]);
+        mma<X3>(vn[i][m], d0, d1, d2, d3, x2, x3);
+        mma<X3>(o[i][m], d0, d1, d2, d3, y2, y3);
       }
     }
   }
   __syncthreads();   // the blocks' inverses
 
-  // acc += (rows of W)(vn)^T for one tile of places: W[8 r + gid][8 s + 2 j, + 1] in shared memory
-  const auto apply = [&](float (&acc)[MT][4], const float (&x)[MT][4], const float *W, float sign) {
+  // acc += x (rows of W)^T for one tile of places: W[8 r + gid][8 s + 2 j, + 1]
+  const auto apply = [&](float (&acc)[MT][4], const float (&x)[MT][4], const float *W) {
     const float2 w = *reinterpret_cast<const float2 *>(W);
-    const Op<X3> b0(sign * w.x), b1(sign * w.y);
+    const Op<X3> b0(w.x), b1(w.y);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
       mma<X3>(acc[m], Op<X3>(x[m][0]), Op<X3>(x[m][2]), Op<X3>(x[m][1]), Op<X3>(x[m][3]), b0, b1);
@@ -431,6 +539,7 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   // ---- (I + L) Vn = beta (V - Kt S0), block by block ----
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
+    if (BT * b >= tiles) break;
     float r[BT][MT][4];
 #pragma unroll
     for (int i = 0; i < BT; ++i) {
@@ -442,63 +551,48 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
           r[i][m][e] = -(e & 1 ? bt.y : bt.x) * vn[BT * b + i][m][e];
           vn[BT * b + i][m][e] = 0.f;
         }
+      if (BT * b + i < tiles) {
 #pragma unroll
-      for (int s = 0; s < BT * b; ++s)
-        apply(r[i], vn[s], s_L + (8 * (BT * b + i) + gid) * LDT + 8 * s + 2 * j, -1.f);
-    }
-#pragma unroll
-    for (int i = 0; i < BT; ++i)
-#pragma unroll
-      for (int s = 0; s <= i; ++s)
-        apply(vn[BT * b + i], r[s], s_M + (8 * (BT * b + i) + gid) * LDB + 8 * s + 2 * j, 1.f);
-  }
-
-  // ---- O = Qt S0 + P Vn, a block of places at a time ----
-  TIn *op = out + row0 * DV + col;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    float o[BT][MT][4];
-#pragma unroll
-    for (int i = 0; i < BT; ++i)
+        for (int s = 0; s < BT * b; ++s)
+          apply(r[i], vn[s], s_L + (8 * (BT * b + i) + gid) * LDT + 8 * s + 2 * j);
+      }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][m][e] = 0.f;
-#pragma unroll
-    for (int a = 0; a < DK / 16; ++a) {
-#pragma unroll
-      for (int i = 0; i < BT; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(
-            s_qt + (8 * (BT * b + i) + gid) * LDK + 16 * a + 4 * j);
-        const Op<X3> b0(x.x), b1(x.y), b2(x.z), b3(x.w);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma<X3>(o[i][m], Op<X3>(s0[4 * a][2 * m]), Op<X3>(s0[4 * a][2 * m + 1]),
-                  Op<X3>(s0[4 * a + 1][2 * m]), Op<X3>(s0[4 * a + 1][2 * m + 1]), b0, b1);
-          mma<X3>(o[i][m], Op<X3>(s0[4 * a + 2][2 * m]), Op<X3>(s0[4 * a + 2][2 * m + 1]),
-                  Op<X3>(s0[4 * a + 3][2 * m]), Op<X3>(s0[4 * a + 3][2 * m + 1]), b2, b3);
-        }
-      }
+        for (int e = 0; e < 4; ++e) r[i][m][e] = operand<X3>(r[i][m][e]);
     }
 #pragma unroll
     for (int i = 0; i < BT; ++i) {
-      const int tile = BT * b + i;
 #pragma unroll
-      for (int s = 0; s <= tile; ++s)
-        apply(o[i], vn[s], s_P + (8 * tile + gid) * LDT + 8 * s + 2 * j, 1.f);
+      for (int s = 0; s <= i; ++s)
+        apply(vn[BT * b + i], r[s], s_M + (8 * (BT * b + i) + gid) * LDB + 8 * s + 2 * j);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = 8 * tile + 2 * j + e;
-        if (t < T) {
-          const bool live = s_anc[t] != 0;
-          float x[E];
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            x[2 * m] = live ? o[i][m][e] : 0.f;
-            x[2 * m + 1] = live ? o[i][m][2 + e] : 0.f;
-          }
-          store_row<E>(op + (int64_t)t * H * DV, x);
+        for (int e = 0; e < 4; ++e) vn[BT * b + i][m][e] = operand<X3>(vn[BT * b + i][m][e]);
+    }
+  }
+
+  // ---- O = Qt S0 + P Vn ----
+  TIn *op = out + row0 * DV + col;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    if (i < tiles) {
+#pragma unroll
+      for (int s = 0; s <= i; ++s) apply(o[i], vn[s], s_P + (8 * i + gid) * LDT + 8 * s + 2 * j);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = 8 * i + 2 * j + e;
+      if (t < T) {
+        const bool live = s_anc[t] != 0;
+        float x[E];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          x[2 * m] = live ? o[i][m][e] : 0.f;
+          x[2 * m + 1] = live ? o[i][m][2 + e] : 0.f;
         }
+        store_row<E>(op + (int64_t)t * H * DV, x);
       }
     }
   }

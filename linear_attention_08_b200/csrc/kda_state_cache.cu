@@ -7,12 +7,12 @@
 // channel, so the rows of a state differ in size by orders of magnitude: each
 // row (key channel) carries its own FP32 scale,
 //
-//   scale = max_v |S[c][v]| / top      (top = 448 for E4M3, 127 for INT8)
-//   code  = round(S[c][v] / scale)     (to nearest, ties to even; clamped to +-top)
+//   scale = max_v |S[c][v]| * (1 / top)   (top = 448 for E4M3, 127 for INT8)
+//   code  = round(S[c][v] / scale)        (to nearest, ties to even; clamped to +-top)
 //   value = code * scale
 //
-// with both quotients correctly rounded, so the codes are reproducible to the
-// bit.  A row of zeros, or one so small that its scale underflows to zero,
+// in FP32, with 1 / top, the product and the quotient each correctly rounded, so
+// that the codes are reproducible to the bit.  A row of zeros, or one so small that its scale underflows to zero,
 // stores zeros; a row that holds an infinity or a NaN stores a NaN scale and
 // reads back as NaN.
 //
@@ -105,7 +105,7 @@ state_store_kernel(const float *__restrict__ states, const int32_t *__restrict__
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       bad += __shfl_xor_sync(0xffffffffu, bad, o);
     }
-    const float scale = bad == 0.f ? m / code_top<E4M3>() : CUDART_NAN_F;
+    const float scale = bad == 0.f ? m * (1.f / code_top<E4M3>()) : CUDART_NAN_F;
     dst[r * V4 + cg] = encode4<E4M3>(x[i], scale);
     if (cg == 0) sc[r] = scale;
   }

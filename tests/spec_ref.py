@@ -107,13 +107,13 @@ E4M3[[0x7F, 0xFF]] = np.nan
 
 
 def quantise(states, kind):
-    """(codes as values, FP32 scales) of FP32 states, one scale per row; quotients
-    rounded to FP32, codes to the nearest, ties to even."""
+    """(codes as values, FP32 scales) of FP32 states, one scale per row (its largest
+    magnitude times 1 / top); every step rounded to FP32, codes to the nearest, ties to even."""
     x = np.asarray(states, np.float32)
     top = np.float32(448.0 if kind == "e4m3" else 127.0)
     with np.errstate(all="ignore"):
         big = np.abs(x).max(-1)
-        scale = np.where(np.isfinite(x).all(-1), big / top, np.float32(np.nan)).astype(np.float32)
+        scale = np.where(np.isfinite(x).all(-1), big * (np.float32(1) / top), np.float32(np.nan)).astype(np.float32)
         y = np.where((scale > 0)[..., None], x / scale[..., None], np.float32(0)).astype(np.float32)
     y = np.clip(y, -top, top)
     if kind == "int8":
