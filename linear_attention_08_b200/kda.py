@@ -7,6 +7,7 @@ is no fallback: if the library is missing or a call fails, this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -352,23 +353,42 @@ def kda_decode_multi(q, k, v, g, beta, state, *, accept_len=None, out=None, dev_
 
 def _want(name, t, shape, dtype, device):
     """Check one argument of the calls below: a dense CUDA tensor of this shape and dtype."""
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or device.type != "cuda":
+    if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be on one CUDA device with the other arguments, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+# Shapes of the calls below, which only read them, by their sizes: building the
+# struct is a tenth of what the host spends on a call.
+_shape = functools.lru_cache(maxsize=1024)(make_shape)
 
 
 def _call(fn, device, stream, *args):
     """Run a library call on the arguments' device and on ``stream`` (None: that
-    device's current stream)."""
-    with torch.cuda.device(device):
-        st = getattr(load(), fn)(*args, _stream(stream))
+    device's current stream).  Pointers are passed as integers and the device is
+    switched only when it is not the current one: small calls are bound by what the
+    host does before the launch."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        st = getattr(_lib or load(), fn)(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            raw = (stream or torch.cuda.current_stream()).cuda_stream
+            st = getattr(load(), fn)(*args, raw)
     if st != KDA_OK:
         raise KdaError(st, fn)
+
+
+def _at(t):
+    """Address of an optional argument."""
+    return None if t is None else t.data_ptr()
 
 
 def _want_tree(k, v, g, beta, state, parents):
@@ -397,9 +417,10 @@ def kda_decode_tree(q, k, v, g, beta, state, *, parents=None, out=None, stream=N
     if out is None:
         out = torch.empty_like(v)
     _want("out", out, v.shape, k.dtype, k.device)
-    shape = make_shape(N, N * T, H, Dk, Dv, 0, code)
-    _call("kda_decode_tree", k.device, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-          _ptr(state), _ptr(parents), _ptr(out), int(T), ctypes.byref(shape))
+    shape = _shape(N, N * T, H, Dk, Dv, 0, code)
+    _call("kda_decode_tree", k.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          g.data_ptr(), beta.data_ptr(), state.data_ptr(), _at(parents), out.data_ptr(), T,
+          ctypes.byref(shape))
     return out
 
 
@@ -415,9 +436,10 @@ def kda_tree_commit(k, v, g, beta, state, accept_node, *, parents=None, state_ou
     if state_out is None:
         state_out = state
     _want("state_out", state_out, state.shape, torch.float32, k.device)
-    shape = make_shape(N, N * T, H, Dk, Dv, 0, code)
-    _call("kda_tree_commit", k.device, stream, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
-          _ptr(state_out), _ptr(parents), _ptr(accept_node), int(T), ctypes.byref(shape))
+    shape = _shape(N, N * T, H, Dk, Dv, 0, code)
+    _call("kda_tree_commit", k.device, stream, k.data_ptr(), v.data_ptr(), g.data_ptr(),
+          beta.data_ptr(), state.data_ptr(), state_out.data_ptr(), _at(parents),
+          accept_node.data_ptr(), T, ctypes.byref(shape))
     return state_out
 
 
@@ -448,24 +470,27 @@ def kda_verify_tree(target_probs, tokens, uniforms, *, draft_probs=None, parents
     _want("accept_node", accept_node, (N,), torch.int32, dev)
     _want("accept_len", accept_len, (N,), torch.int32, dev)
     _want("out_tokens", out_tokens, (N, T1), torch.int32, dev)
-    _call("kda_verify_tree", dev, stream, _ptr(target_probs), _ptr(draft_probs), _ptr(tokens),
-          _ptr(parents), _ptr(uniforms), _ptr(accept_node), _ptr(accept_len), _ptr(out_tokens),
-          int(N), int(T), int(V), code)
+    _call("kda_verify_tree", dev, stream, target_probs.data_ptr(), _at(draft_probs),
+          tokens.data_ptr(), _at(parents), uniforms.data_ptr(), accept_node.data_ptr(),
+          accept_len.data_ptr(), out_tokens.data_ptr(), N, T, V, code)
     return accept_node, accept_len, out_tokens
+
+
+_CACHE_CODES = {torch.float8_e4m3fn: KDA_CACHE_E4M3, torch.int8: KDA_CACHE_INT8}
 
 
 def _want_cache(states, slots, cache, scales):
     n, H, Dk, Dv = states.shape
     dev = states.device
-    codes = {torch.float8_e4m3fn: KDA_CACHE_E4M3, torch.int8: KDA_CACHE_INT8}
-    if cache.dtype not in codes:
+    code = _CACHE_CODES.get(cache.dtype)
+    if code is None:
         raise TypeError(f"cache must be float8_e4m3fn or int8, got {cache.dtype}")
     num_slots = cache.shape[0]
     _want("states", states, (n, H, Dk, Dv), torch.float32, dev)
     _want("slots", slots, (n,), torch.int32, dev)
     _want("cache", cache, (num_slots, H, Dk, Dv), cache.dtype, dev)
     _want("scales", scales, (num_slots, H, Dk), torch.float32, dev)
-    return int(num_slots), codes[cache.dtype], make_shape(n, n, H, Dk, Dv, 0, KDA_DTYPE_F32)
+    return num_slots, code, _shape(n, n, H, Dk, Dv, 0, KDA_DTYPE_F32)
 
 
 def kda_state_store(states, slots, cache, scales, *, stream=None):
@@ -475,8 +500,8 @@ def kda_state_store(states, slots, cache, scales, *, stream=None):
     (float8_e4m3fn or int8), scales [num_slots, H, Dk] FP32.  Returns (cache,
     scales)."""
     num_slots, code, shape = _want_cache(states, slots, cache, scales)
-    _call("kda_state_store", states.device, stream, _ptr(states), _ptr(slots), _ptr(cache),
-          _ptr(scales), num_slots, code, ctypes.byref(shape))
+    _call("kda_state_store", states.device, stream, states.data_ptr(), slots.data_ptr(),
+          cache.data_ptr(), scales.data_ptr(), num_slots, code, ctypes.byref(shape))
     return cache, scales
 
 
@@ -487,8 +512,8 @@ def kda_state_load(cache, scales, slots, *, states=None, stream=None):
         states = torch.empty(slots.numel(), *cache.shape[1:], dtype=torch.float32,
                              device=cache.device)
     num_slots, code, shape = _want_cache(states, slots, cache, scales)
-    _call("kda_state_load", states.device, stream, _ptr(cache), _ptr(scales), _ptr(slots),
-          _ptr(states), num_slots, code, ctypes.byref(shape))
+    _call("kda_state_load", states.device, stream, cache.data_ptr(), scales.data_ptr(),
+          slots.data_ptr(), states.data_ptr(), num_slots, code, ctypes.byref(shape))
     return states
 
 
