@@ -32,18 +32,12 @@ constexpr int kCacheThreads = 256;
 
 template <bool E4M3> __device__ __forceinline__ float code_top() { return E4M3 ? 448.f : 127.f; }
 
-// Four codes of one row, packed in memory order.
-template <bool E4M3> __device__ __forceinline__ uint32_t encode4(float4 x, float scale) {
+// Four codes of one row, packed in memory order, by the quotients.
+template <bool E4M3> __device__ __noinline__ uint32_t encode4_exact(float4 x, float scale) {
   const float top = code_top<E4M3>();
-  float y[4] = {0.f, 0.f, 0.f, 0.f};
-  if (scale > 0.f) {   // false for a NaN scale too
-    y[0] = x.x / scale;
-    y[1] = x.y / scale;
-    y[2] = x.z / scale;
-    y[3] = x.w / scale;
+  float y[4] = {x.x / scale, x.y / scale, x.z / scale, x.w / scale};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = fminf(fmaxf(y[i], -top), top);
-  }
+  for (int i = 0; i < 4; ++i) y[i] = fminf(fmaxf(y[i], -top), top);
   if (E4M3) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
@@ -52,6 +46,52 @@ template <bool E4M3> __device__ __forceinline__ uint32_t encode4(float4 x, float
   uint32_t r = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(y[i]) << (8 * i);
+  return r;
+}
+
+// Four codes from products with one factor.  INT8: 1.5 * 2^23 + x f, rounded once,
+// holds the nearest integer in its low byte.
+template <bool E4M3> __device__ __forceinline__ uint32_t encode4_by(float4 x, float f) {
+  if (E4M3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x.x * f, x.y * f), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x.z * f, x.w * f), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  }
+  constexpr float kBase = 12582912.f;
+  const uint32_t lo = __byte_perm(__float_as_uint(__fmaf_rn(x.x, f, kBase)),
+                                  __float_as_uint(__fmaf_rn(x.y, f, kBase)), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(__fmaf_rn(x.z, f, kBase)),
+                                  __float_as_uint(__fmaf_rn(x.w, f, kBase)), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// The codes are those of the rounded quotients x / scale, at a third of their cost:
+// with factors at least 5 * 2^-24 (relative) below and above 1 / scale, x times one
+// of them lies on each side of the rounded quotient (its own rounding, the
+// reciprocal's and the product's are 4 * 2^-24 together), and rounding to codes is
+// monotone.  Where both give one code, it is the quotient's; else (about one vector
+// of four in 10^5) the quotients are formed.
+struct Factor {
+  float lo, hi;
+  bool sure;             // the scale is large enough for its reciprocal to be a normal number
+  __device__ __forceinline__ explicit Factor(float scale) {
+    const float r = __frcp_rn(scale);
+    lo = r * (1.f - 0x1p-21f);
+    hi = r * (1.f + 0x1p-21f);
+    sure = scale >= 0x1p-100f;
+  }
+};
+template <bool E4M3>
+__device__ __forceinline__ uint32_t encode4(float4 x, float scale, const Factor &f) {
+  const uint32_t a = encode4_by<E4M3>(x, f.lo), b = encode4_by<E4M3>(x, f.hi);
+  if (f.sure && a == b) return a;
+  return scale > 0.f ? encode4_exact<E4M3>(x, scale) : 0u;   // false for a NaN scale too
+}
+
+// The larger of two magnitudes, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -97,16 +137,17 @@ state_store_kernel(const float *__restrict__ states, const int32_t *__restrict__
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     const int r = rg + i * RPP;
-    float m = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
-    // fmaxf drops NaNs, and infinity * 0 is one: any of the two makes the scale NaN
-    float bad = x[i].x * 0.f + x[i].y * 0.f + x[i].z * 0.f + x[i].w * 0.f;
+    // The bits of non-negative numbers are ordered like them, infinity and NaN last.
+    uint32_t m = __float_as_uint(max_nan(max_nan(fabsf(x[i].x), fabsf(x[i].y)),
+                                         max_nan(fabsf(x[i].z), fabsf(x[i].w))));
+    if (V4 == 32) {
+      m = __reduce_max_sync(0xffffffffu, m);
+    } else {
 #pragma unroll
-    for (int o = 1; o < V4; o <<= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      bad += __shfl_xor_sync(0xffffffffu, bad, o);
+      for (int o = 1; o < V4; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-    const float scale = bad == 0.f ? m * (1.f / code_top<E4M3>()) : CUDART_NAN_F;
-    dst[r * V4 + cg] = encode4<E4M3>(x[i], scale);
+    const float scale = m < 0x7f800000u ? __uint_as_float(m) * (1.f / code_top<E4M3>()) : CUDART_NAN_F;
+    dst[r * V4 + cg] = encode4<E4M3>(x[i], scale, Factor(scale));
     if (cg == 0) sc[r] = scale;
   }
 }
