@@ -59,56 +59,137 @@ template <> __device__ __forceinline__ void unpack16<__nv_bfloat16>(uint4 x, flo
   }
 }
 
-// What is left of a context's target distribution after its refusals.
+// What is left of a context's target distribution after its refusals, by case:
+// kWhole: none; kMinus: one, max(p - d, 0); kMany: several with a draft;
+// kGone: without a draft, the refused tokens' elements are zero.
+enum Mode { kWhole, kMinus, kMany, kGone };
 struct Rest {
   bool draft;             // refusals subtract the draft's row (else zero a token)
   int m;                  // refusals so far
-  const double *inv;      // 1 / R before each of them
+  const double *inv;      // 1 / R before each of them (1 before the first)
   const int32_t *gone;    // the refused tokens
-  __device__ __forceinline__ double of(float p, float d, int token) const {
-    double r = (double)p;
-    if (draft) {
-      for (int l = 0; l < m; ++l) r = fmax(r * inv[l] - (double)d, 0.0);
-    } else {
-      for (int l = 0; l < m; ++l) r = gone[l] == token ? 0.0 : r;
+  __device__ __forceinline__ Mode mode() const {
+    return m == 0 ? kWhole : !draft ? kGone : m == 1 ? kMinus : kMany;
+  }
+  // r of W neighbouring elements from `at` on.
+  template <int MODE, int W>
+  __device__ __forceinline__ void of(const float (&p)[W], const float (&d)[W], int at,
+                                     double (&r)[W]) const {
+#pragma unroll
+    for (int e = 0; e < W; ++e) r[e] = (double)p[e];
+    if (MODE == kMinus) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) r[e] = p[e] > d[e] ? r[e] - (double)d[e] : 0.0;
+    } else if (MODE == kMany) {
+#pragma unroll 1
+      for (int l = 0; l < m; ++l) {
+        const double x = inv[l];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          r[e] = r[e] * x - (double)d[e];
+          r[e] = r[e] > 0.0 ? r[e] : 0.0;
+        }
+      }
+    } else if (MODE == kGone) {
+#pragma unroll 1
+      for (int l = 0; l < m; ++l) {
+        const int x = gone[l] - at;
+#pragma unroll
+        for (int e = 0; e < W; ++e) r[e] = x == e ? 0.0 : r[e];
+      }
     }
-    return r;
   }
 };
 
-// Sum of the rest over [lo, hi), over the calling lanes' strided elements.
-// A row starts where its element type aligns, no more: 16-byte loads when both
-// rows allow them, else single elements, several in flight.
-template <typename P>
-__device__ __forceinline__ double rest_sum(const P *p, const P *d, const Rest &rest, int lo,
-                                           int hi, int first, int stride) {
-  constexpr int V = VecOf<P>::N;
+// W neighbouring elements as one load gives them (one, or 16 bytes), and as floats.
+template <typename P, int W> struct Raw {
+  uint4 x;
+  __device__ __forceinline__ void load(const P *p) { x = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&f)[W]) const { unpack16<P>(x, f); }
+};
+template <typename P> struct Raw<P, 1> {
+  P x;
+  __device__ __forceinline__ void load(const P *p) { x = __ldg(p); }
+  __device__ __forceinline__ void clear() { x = from_f32<P>(0.f); }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(x); }
+};
+
+// Sum of the rest over [lo, hi) over the calling lanes' strided loads of W
+// elements, B of them in flight; hi - lo is a multiple of W.
+template <typename P, int MODE, int W>
+__device__ __forceinline__ double sum_w(const P *p, const P *d, const Rest &rest, int lo, int hi,
+                                        int lane) {
+  constexpr int B = MODE == kMany ? 1 : W == 1 ? 8 : 4;
+  constexpr bool D = MODE == kMinus || MODE == kMany;
   double acc = 0.0;
-  const bool sub = rest.draft && rest.m > 0;
-  if (((reinterpret_cast<uintptr_t>(p + lo) | (sub ? reinterpret_cast<uintptr_t>(d + lo) : 0)) & 15u) == 0) {
-    const int nv = (hi - lo) / V;
-    const uint4 *p4 = reinterpret_cast<const uint4 *>(p + lo);
-    const uint4 *d4 = reinterpret_cast<const uint4 *>(d + lo);
-#pragma unroll 4
-    for (int i = first; i < nv; i += stride) {
-      float a[V], b[V];
-      unpack16<P>(__ldg(p4 + i), a);
-      if (sub) unpack16<P>(__ldg(d4 + i), b);
+#pragma unroll 1
+  for (int i = lo + lane * W; i < hi; i += B * 32 * W) {
+    Raw<P, W> a[B], b[B];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc += rest.of(a[e], sub ? b[e] : 0.f, lo + i * V + e);
+    for (int j = 0; j < B; ++j) {
+      const int at = i + j * 32 * W;
+      if (at < hi) {
+        a[j].load(p + at);
+        if (D) b[j].load(d + at);
+      } else {
+        a[j].clear();
+        if (D) b[j].clear();
+      }
     }
-    for (int i = lo + nv * V + first; i < hi; i += stride)
-      acc += rest.of(to_f32(p[i]), sub ? to_f32(d[i]) : 0.f, i);
-  } else {
-#pragma unroll 8
-    for (int i = lo + first; i < hi; i += stride)
-      acc += rest.of(to_f32(p[i]), sub ? to_f32(d[i]) : 0.f, i);
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      float x[W], y[W];
+      double r[W];
+      a[j].get(x);
+      if (D) b[j].get(y);
+      rest.of<MODE, W>(x, y, i + j * 32 * W, r);
+#pragma unroll
+      for (int o = 1; o < W; o <<= 1)      // pairs first: short chains of FP64 additions
+#pragma unroll
+        for (int e = 0; e + o < W; e += 2 * o) r[e] += r[e + o];
+      acc += r[0];
+    }
   }
   return acc;
 }
 
+// The same with 16-byte loads where the rows allow them (a row starts where its
+// element type aligns, no more), else, and behind the last whole one, by elements.
+template <typename P, int MODE>
+__device__ __noinline__ double sum_mode(const P *p, const P *d, const Rest &rest, int lo, int hi,
+                                        int lane) {
+  constexpr int V = VecOf<P>::N;
+  constexpr bool D = MODE == kMinus || MODE == kMany;
+  uintptr_t bits = reinterpret_cast<uintptr_t>(p + lo);
+  if (D) bits |= reinterpret_cast<uintptr_t>(d + lo);
+  const int whole = (bits & 15u) == 0 ? (hi - lo) / V * V : 0;
+  double acc = 0.0;
+  if (whole) acc = sum_w<P, MODE, V>(p, d, rest, lo, lo + whole, lane);
+  if (lo + whole < hi) acc += sum_w<P, MODE, 1>(p, d, rest, lo + whole, hi, lane);
+  return acc;
+}
 template <typename P>
-__global__ void __launch_bounds__(kVThreads)
+__device__ __forceinline__ double rest_sum(const P *p, const P *d, const Rest &rest, int lo,
+                                           int hi, int lane) {
+  switch (rest.mode()) {
+    case kWhole: return sum_mode<P, kWhole>(p, d, rest, lo, hi, lane);
+    case kMinus: return sum_mode<P, kMinus>(p, d, rest, lo, hi, lane);
+    case kMany: return sum_mode<P, kMany>(p, d, rest, lo, hi, lane);
+    default: return sum_mode<P, kGone>(p, d, rest, lo, hi, lane);
+  }
+}
+// One element's.
+__device__ __forceinline__ double rest_one(const Rest &rest, float p, float d, int at) {
+  const float a[1] = {p}, b[1] = {d};
+  double r[1];
+  if (rest.draft) rest.of<kMany, 1>(a, b, at, r);
+  else rest.of<kGone, 1>(a, b, at, r);
+  return r[0];
+}
+
+template <typename P>
+__global__ void __launch_bounds__(kVThreads, 2)
 verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
                    const int32_t *__restrict__ tokens, const int32_t *__restrict__ parents,
                    const float *__restrict__ uniforms, int32_t *__restrict__ accept_node,
@@ -123,8 +204,8 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   __shared__ int s_last[kVWarps];
 
   cg::cluster_group cluster = cg::this_cluster();
-  cluster.barrier_arrive();   // the others' shared memory exists once all have started
   const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  if (CS > 1) cluster.barrier_arrive();   // the others' shared memory exists once all have started
   const int64_t n = blockIdx.x / CS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const P *trow = target + n * (T + 1) * (int64_t)vocab;
@@ -150,7 +231,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     s_d[tid] = drow && up >= -1 && in ? to_f32(drow[(int64_t)(up + 1) * vocab + x]) : 1.f;
   }
   __syncthreads();
-  cluster.barrier_wait();
+  if (CS > 1) cluster.barrier_wait();
 
   // Every thread of the cluster takes the same decisions from here on.
   Rest rest{drow != nullptr, 0, s_inv, s_gone};
@@ -161,7 +242,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     const int w = rank * kVWarps + warp;
     double x = rest_sum<P>(trow + (int64_t)(cur + 1) * vocab,
                            rest.draft ? drow + (int64_t)min(cur + 1, T - 1) * vocab : nullptr, rest,
-                           bound(w), bound(w + 1), lane, 32);
+                           bound(w), bound(w + 1), lane);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lane == 0) s_warp[warp] = x;
@@ -173,7 +254,8 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
       for (int i = 0; i < kVWarps; ++i) t += s_warp[i];
       cluster.map_shared_rank(&s_tot[buf][0], tid)[rank] = t;
     }
-    cluster.sync();
+    if (CS > 1) cluster.sync();
+    else __syncthreads();
     double t = 0.0;
     for (int i = 0; i < CS; ++i) t += s_tot[buf][i];
     return t;
@@ -182,7 +264,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   for (int i = 0; i < T; ++i) {
     if (s_par[i] != cur) continue;
     if (rest.draft && rest.m > 0) R = sum_rest();
-    const double r = rest.of(s_p[i], s_d[i], s_tok[i]);
+    const double r = rest_one(rest, s_p[i], s_d[i], s_tok[i]);
     if (r > 0.0 && (double)s_u[i] * R * (double)s_d[i] < r) {
       if (tid == 0) s_path[count] = i;
       ++count;
@@ -249,7 +331,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   double mine = 0.0;
   int last = -1;
   for (int i = a; i < b; ++i) {
-    const double r = rest.of(to_f32(p[i]), d ? to_f32(d[i]) : 0.f, i);
+    const double r = rest_one(rest, to_f32(p[i]), d ? to_f32(d[i]) : 0.f, i);
     mine += r;
     if (r > 0.0) last = i;
   }
@@ -275,7 +357,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   int hit = INT32_MAX;
   double c = start + (incl - mine);
   for (int i = a; i < b; ++i) {
-    const double r = rest.of(to_f32(p[i]), d ? to_f32(d[i]) : 0.f, i);
+    const double r = rest_one(rest, to_f32(p[i]), d ? to_f32(d[i]) : 0.f, i);
     c += r;
     if (r > 0.0 && c > border) { hit = i; break; }
   }
@@ -297,11 +379,12 @@ cudaError_t launch_verify_tree(bool bf16, const void *target, const void *draft,
                                const float *uniforms, int32_t *accept_node, int32_t *accept_len,
                                int32_t *out_tokens, int N, int T, int vocab, int num_sms,
                                cudaStream_t stream) {
-  // CTAs per sequence: as many as keep the grid within four CTAs per SM (a
-  // lone sequence is bound by what its few SMs can load), at most the portable
-  // cluster size.
+  // CTAs per sequence: as many as keep the grid within the two CTAs that an SM
+  // holds (a lone sequence is bound by what its few SMs can load) and leave each a
+  // 16-byte load per thread, at most the portable cluster size.
   int cs = kVMaxCluster;
-  while (cs > 1 && (int64_t)N * cs > 4 * (int64_t)num_sms) cs >>= 1;
+  const int least = kVThreads * (bf16 ? VecOf<__nv_bfloat16>::N : VecOf<float>::N);
+  while (cs > 1 && ((int64_t)N * cs > 2 * (int64_t)num_sms || vocab <= (cs / 2) * least)) cs >>= 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)N * cs));
   cfg.blockDim = dim3(kVThreads);
