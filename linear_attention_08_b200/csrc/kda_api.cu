@@ -25,6 +25,11 @@ cudaError_t launch_decode_tree(int dtype, int dk, int dv, const void *q, const v
                                const void *v, const float *g, const float *beta,
                                const float *state, const int32_t *parents, void *out, int T,
                                int64_t units, int H, cudaStream_t stream);
+bool decode_tree_tc_supported(int dtype, int dk, int dv);
+cudaError_t launch_decode_tree_tc(const void *q, const void *k, const void *v, const float *g,
+                                  const float *beta, const float *state, const int32_t *parents,
+                                  void *out, int T, int64_t units, int H, int32_t *dev_status,
+                                  cudaStream_t stream);
 cudaError_t launch_tree_commit(int dtype, int dk, int dv, const void *k, const void *v,
                                const float *g, const float *beta, const float *state,
                                float *state_out, const int32_t *parents,
@@ -613,6 +618,10 @@ kda_status kda_decode_tree(const void *q, const void *k, const void *v, const fl
       overlaps(out, n_out, g, n_g) || overlaps(out, n_out, beta, (size_t)T * H * 4) ||
       overlaps(out, n_out, parents, (size_t)T * 4))
     return KDA_ERR_INVALID_ARGUMENT;
+  if (decode_tree_tc_supported(s->qkv_dtype, s->head_dim_k, s->head_dim_v))
+    return cuda_status(launch_decode_tree_tc(q, k, v, g, beta, state, parents, out, nodes_per_seq,
+                                             units, s->num_heads, s->dev_status,
+                                             reinterpret_cast<cudaStream_t>(stream)));
   return cuda_status(launch_decode_tree(s->qkv_dtype, s->head_dim_k, s->head_dim_v, q, k, v, g,
                                         beta, state, parents, out, nodes_per_seq, units,
                                         s->num_heads, reinterpret_cast<cudaStream_t>(stream)));

@@ -137,7 +137,7 @@ template <> struct MaskOf<8> { using T = unsigned long long; };
 // NT: tiles of 8 places (places past T are empty ones).
 template <int DK, int DV, int NT, typename TIn> struct TreeCfg {
   static constexpr bool X3 = sizeof(TIn) == 4;
-  static constexpr int MT = NT == 8 || X3 ? 1 : 2;  // 16-column tiles per warp (registers)
+  static constexpr int MT = 1;  // 16-column tiles per warp (registers)
   static constexpr int E = 2 * MT;                  // value columns, or key channels, per lane
   static constexpr int WARPS = DV / (16 * MT);
   static constexpr int THREADS = 32 * WARPS;
