@@ -45,6 +45,7 @@ template <int TP> struct TreeTc {
   static constexpr int THREADS = WORKERS + 32;
   static constexpr int TH = TP < 32 ? TP : 32;           // tokens in X at a time (a part)
   static constexpr int NH = TP / TH;
+  static constexpr int OB = TP / kBlk / WG;              // blocks of outputs per warpgroup
   static constexpr int XR = 2 * TH;                      // rows of X
   static constexpr int ROWS = 2 * TP;                    // rows of [KK; P], part by part
   // shared memory, bytes
@@ -136,6 +137,12 @@ __device__ __forceinline__ uint64_t step_desc(uint64_t first, int rows, int s) {
 __device__ __forceinline__ uint32_t tile32(int rows, int row, int col) {
   return (uint32_t)((col >> 5) * rows * 128 + row * 128 + ((((col & 31) >> 2) ^ (row & 7)) << 4) +
                     (col & 3) * 4);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Barrier of the computing threads with a common "or".
@@ -337,6 +344,24 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       }
       tc::fence_after_sync();
     };
+    // A unit's outputs: blocks hw, hw + WG, ... of its tokens.
+    float o[C::OB][kBlk];
+    unsigned long long o_all = 0;
+    __nv_bfloat16 *o_at = out;
+    const int64_t o_step = (int64_t)H * kD;
+    const auto put_out = [&] {
+#pragma unroll
+      for (int e = 0; e < C::OB; ++e) {
+        const int t0 = kBlk * (hw + C::WG * e), left = T - t0;
+        const uint32_t live = (uint32_t)(o_all >> t0);
+        __nv_bfloat16 *at = o_at + t0 * o_step;
+#pragma unroll
+        for (int j = 0; j < kBlk; ++j) {
+          if (j < left) *at = __float2bfloat16_rn((live >> j) & 1 ? o[e][j] : 0.f);
+          at += o_step;
+        }
+      }
+    };
     uint32_t i = 0;
     for (int64_t u = blockIdx.x; u < units; u += G, ++i) {
       const uint32_t ph = i & 1;
@@ -390,7 +415,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       tc::fence_before_sync();
       // (every thread is past the last unit's [KK; P], too, where Kh will be)
       if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
-      if (tid == 0) {
+      if (tid == 96) {
         tc::fence_after_sync();
         for (int b = 0; b < nb; ++b)
 #pragma unroll
@@ -401,6 +426,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           }
         tc::mma_commit(bar_at(kMmaG));
       }
+      __syncwarp();
       pend |= 1u << kMmaG;
       done(kMmaG);
 
@@ -409,7 +435,10 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
 #pragma unroll
       for (int hf = 0; hf < C::NH; ++hf) {
         if (hf > 0 && hf >= nh) break;
-        if (hf > 0) done(kMmaB);           // the products before have read X
+        if (hf > 0) {                      // the products before have read X
+          done(kMmaA);
+          done(kMmaB);
+        }
         const int j0 = kBlk * hw, t0 = C::TH * hf + j0;
         if (t0 < kBlk * nb) {
           float Gt[kBlk];
@@ -421,7 +450,8 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
 #pragma unroll
           for (int j = 0; j < kBlk; ++j) {
             const float kv = __bfloat162float(rk[(t0 + j) * kD]), qv = __bfloat162float(rq[(t0 + j) * kD]);
-            const float down = __expf(Gt[j]), d = kv * __expf(-Gt[j]);
+            const float e = Gt[j] * 1.44269504f;     // to a power of two
+            const float down = exp2_approx(e), d = kv * exp2_approx(-e);
             wide |= !(fabsf(Gt[j]) <= kGamBound && fabsf(d) < kFactorBound);
             const uint32_t at = (within ^ ((j & 7) << 4)) + j * 128;
             *reinterpret_cast<float *>(xt + at) = to_tf32(kv * down);
@@ -434,27 +464,32 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         else tc::fence_smem_to_async();
         tc::fence_before_sync();
         if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
-        if (tid == 0) {
+        // Two threads issue: it takes one about 70 cycles per product.
+        if (tid == 32) {
           tc::fence_after_sync();
 #pragma unroll
           for (int s = 0; s < kD / 8; ++s)
             mma_tf32_ss(tmem + C::D2 + C::TH * hf, step_desc(x_desc, C::XR, s),
                         step_desc(kh_desc, TP, s), idesc_tf32(128, C::TH * (hf + 1)), s > 0);
-          if (C::NH == 1) tc::mma_commit(bar_at(kMmaA));
+          tc::mma_commit(bar_at(kMmaA));
+        } else if (tid == 64) {
+          tc::fence_after_sync();
 #pragma unroll
           for (int s = 0; s < kD / 8; ++s)
             mma_tf32_ts(tmem + C::D1 + C::XR * hf, tmem + C::S + 8 * s,
                         step_desc(x_desc, C::XR, s), idesc_tf32(128, C::XR), s > 0);
           tc::mma_commit(bar_at(kMmaB));
         }
-        pend |= (C::NH == 1 ? 1u << kMmaA : 0u) | 1u << kMmaB;
+        __syncwarp();
+        pend |= 1u << kMmaA | 1u << kMmaB;
+        if (hf == 0 && i > 0) put_out();   // the last unit's outputs, while the products run
       }
       if (aborted) break;
 
       // ---- KK and P, masked.  Row of token t in the tile: XR (t / TH) + t % TH, and TH
       //      below it for P ----
       const bool pairwise = s_wide[ph] != 0;
-      done(C::NH == 1 ? kMmaA : kMmaB);
+      done(kMmaA);
       if (tid == 0) s_wide[ph ^ 1] = 0;
       if (!pairwise) {
 #pragma unroll
@@ -526,7 +561,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       }
       tc::fence_smem_to_async();
       bad |= !wait_timed(bars + kFullV, ph, wait_ns);
-      if (C::NH == 1) done(kMmaB);
+      done(kMmaB);
       tc::fence_before_sync();
       if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
       tc::fence_after_sync();
@@ -581,24 +616,18 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       pend |= 1u << kMmaO;
       done(kMmaO);
 
-      // ---- the outputs ----
-      __nv_bfloat16 *op = out + row0 * kD + col;
-      for (int b = hw; kBlk * b < T; b += C::WG) {
-        float o[kBlk];
-        if (b < nb) {
-          tc::tmem_ld16(tl + C::D1 + (uint32_t)(C::XR * (kBlk * b / C::TH) + C::TH + kBlk * b % C::TH), o);
-          tc::tmem_wait_ld();
-        } else {
+      // ---- the outputs, kept until the next unit's products run ----
 #pragma unroll
-          for (int j = 0; j < kBlk; ++j) o[j] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < kBlk; ++j)
-          if (kBlk * b + j < T)
-            op[(int64_t)(kBlk * b + j) * H * kD] =
-                __float2bfloat16_rn((all >> (kBlk * b + j)) & 1 ? o[j] : 0.f);
+      for (int e = 0; e < C::OB; ++e) {
+        const int b = hw + C::WG * e;
+        if (b < nb)
+          tc::tmem_ld16(tl + C::D1 + (uint32_t)(C::XR * (kBlk * b / C::TH) + C::TH + kBlk * b % C::TH), o[e]);
       }
+      tc::tmem_wait_ld();
+      o_all = all;
+      o_at = out + row0 * kD + col;
     }
+    if (i > 0 && !aborted) put_out();
     if (aborted || bad) {
       report(dev_status, KDA_ERR_TIMEOUT);
       *s_quit = 1;

@@ -19,70 +19,82 @@ namespace kda {
 namespace {
 
 constexpr int kGroup = 8;        // tokens staged at a time
-constexpr int kMaxNodes = 64;
+
+// Value columns of one CTA.
+template <int DV> constexpr int kCols = DV < 64 ? DV : 64;
 
 template <int DK, int DV, typename TIn>
-__global__ void __launch_bounds__(2 * DV, 512 / (2 * DV))
+__global__ void __launch_bounds__(2 * kCols<DV>, 640 / (2 * kCols<DV>))
 tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
                    const float *__restrict__ g, const float *__restrict__ beta,
                    const float *state, float *state_out, const int32_t *__restrict__ parents,
                    const int32_t *__restrict__ accept_node, int T, int H) {
-  constexpr int THREADS = 2 * DV;             // 16 columns per warp
+  constexpr int COLS = kCols<DV>, PARTS = DV / COLS;
+  constexpr int THREADS = 2 * COLS;           // 16 columns per warp
   constexpr int V4 = DV / 4;
   constexpr int ROWS = DK / 8;                // float4s per thread
   __shared__ float2 s_ak[kGroup][DK];         // (alpha, k)
-  __shared__ float s_v[kGroup][DV];
+  __shared__ float s_v[kGroup][COLS];
   __shared__ float s_b[kGroup];
-  __shared__ int32_t s_par[kMaxNodes];
-  __shared__ int32_t s_path[kMaxNodes];
-  __shared__ int32_t s_len;
 
-  const int64_t unit = blockIdx.x;
+  const int64_t unit = blockIdx.x / PARTS;
+  const int part = blockIdx.x % PARTS;
   const int n = (int)(unit / H), h = (int)(unit % H);
   const int tid = threadIdx.x, lane = tid & 31;
   const int cg = 4 * (tid >> 5) + (lane & 3);  // float4 column
   const int ks = lane >> 2;                    // rows ks, ks + 8, ...
 
-  const int32_t node = accept_node[n];
+  const int32_t node = __ldg(accept_node + n);
+  int32_t up0 = -2, up1 = -2;                  // predecessors of places lane and lane + 32
+  if (parents) {
+    if (lane < T) up0 = __ldg(parents + (int64_t)n * T + lane);
+    if (lane + 32 < T) up1 = __ldg(parents + (int64_t)n * T + lane + 32);
+  }
+  // In place, a sequence without an accepted token is not touched; otherwise the
+  // state is loaded before anything is known of the path.
   const bool named = node >= 0 && node < T;
-  if (!named && state_out == state) return;
-  const float4 *src = reinterpret_cast<const float4 *>(state) + unit * (DK * V4);
-  float4 *dst = reinterpret_cast<float4 *>(state_out) + unit * (DK * V4);
+  if (state_out == state && !named) return;
+  const float4 *src = reinterpret_cast<const float4 *>(state) + unit * (DK * V4) + part * (COLS / 4);
+  float4 *dst = reinterpret_cast<float4 *>(state_out) + unit * (DK * V4) + part * (COLS / 4);
   float4 s[ROWS];
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) s[i] = __ldcs(src + (ks + 8 * i) * V4 + cg);
 
-  if (parents)
-    for (int i = tid; i < T; i += THREADS) s_par[i] = parents[(int64_t)n * T + i];
-  __syncthreads();
-  if (tid == 0) {
-    // token -> state; a parent out of place means that the path holds an empty one
-    int len = 0, i = named ? node : -1;
-    while (i >= 0) {
-      s_path[len++] = i;                       // at most T steps: i decreases
-      const int up = parents ? s_par[i] : i - 1;
-      if (up < -1 || up >= i) { len = 0; break; }
+  // The path as a set of places (a token's place is above its predecessor's), found
+  // by every warp for itself: no shared memory, no barrier.
+  unsigned long long path = 0;
+  if (named && parents) {
+    for (int i = node; i >= 0;) {              // at most T steps: i decreases
+      path |= 1ull << i;
+      const int up = __shfl_sync(0xffffffffu, i < 32 ? up0 : up1, i & 31);
+      if (up < -1 || up >= i) { path = 0; break; }   // it holds an empty place
       i = up;
     }
-    s_len = len;
+  } else if (named) {
+    path = ~0ull >> (63 - node);
   }
-  __syncthreads();
-  const int len = s_len;
-  if (len == 0 && state_out == state) return;
+  if (state_out == state && path == 0) return;
 
-  for (int base = 0; base < len; base += kGroup) {
-    const int m = min(kGroup, len - base);
-    if (base) __syncthreads();
-    for (int e = tid; e < m * DK; e += THREADS) {
-      const int j = e / DK, c = e % DK;
-      const int64_t row = ((int64_t)n * T + s_path[len - 1 - base - j]) * H + h;
-      s_ak[j][c] = make_float2(expf(g[row * DK + c]), to_f32(k[row * DK + c]));
-    }
-    for (int e = tid; e < m * DV; e += THREADS) {
-      const int j = e / DV, c = e % DV;
-      const int64_t row = ((int64_t)n * T + s_path[len - 1 - base - j]) * H + h;
-      s_v[j][c] = to_f32(v[row * DV + c]);
-      if (c == 0) s_b[j] = beta[row];
+  const int64_t row0 = (int64_t)n * T * H + h;
+  for (bool first = true; path != 0; first = false) {
+    const int m = min(kGroup, __popcll(path));
+    if (!first) __syncthreads();
+    const unsigned long long all = path;
+#pragma unroll
+    for (int e0 = 0; e0 < DK + COLS; e0 += THREADS) {
+      const int e = e0 + tid;
+      unsigned long long rest = all;
+#pragma unroll 4
+      for (int j = 0; j < kGroup; ++j) {
+        if (j < m && e < DK + COLS) {
+          const int64_t row = row0 + (int64_t)(__ffsll(rest) - 1) * H;
+          if (e < DK) s_ak[j][e] = make_float2(expf(g[row * DK + e]), to_f32(k[row * DK + e]));
+          else s_v[j][e - DK] = to_f32(v[row * DV + part * COLS + (e - DK)]);
+          if (e == 0) s_b[j] = beta[row];
+        }
+        rest &= rest - 1;
+      }
+      path = rest;
     }
     __syncthreads();
     for (int j = 0; j < m; ++j) {
@@ -126,7 +138,7 @@ cudaError_t launch_t(int dk, int dv, const void *k, const void *v, const float *
                      int H, cudaStream_t stream) {
 #define KDA_TC(DK_, DV_)                                                                         \
   if (dk == DK_ && dv == DV_) {                                                                  \
-    tree_commit_kernel<DK_, DV_, TIn><<<(unsigned)units, 2 * DV_, 0, stream>>>(                  \
+    tree_commit_kernel<DK_, DV_, TIn><<<(unsigned)(units * (DV_ / kCols<DV_>)), 2 * kCols<DV_>, 0, stream>>>( \
         (const TIn *)k, (const TIn *)v, g, beta, state, state_out, parents, accept_node, T, H);  \
     return cudaGetLastError();                                                                   \
   }
