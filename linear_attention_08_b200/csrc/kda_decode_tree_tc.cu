@@ -139,6 +139,17 @@ __device__ __forceinline__ uint32_t tile32(int rows, int row, int col) {
                     (col & 3) * 4);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -174,7 +185,8 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
   uint64_t *bars = reinterpret_cast<uint64_t *>(sp + C::BAR);
   volatile int *s_quit = reinterpret_cast<int *>(sp + C::QUIT);
   volatile int *s_wide = reinterpret_cast<int *>(sp + C::WIDE);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be uniform
   const int64_t G = gridDim.x;
   const auto bar_at = [&](int b) { return sb + C::BAR + 8 * b; };
 
@@ -191,7 +203,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sp + C::SLOT);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sp + C::SLOT), 0);
 
   if (warp == C::WORKERS / 32) {
     // ------------------------------------------------------------ producer
@@ -415,7 +427,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       tc::fence_before_sync();
       // (every thread is past the last unit's [KK; P], too, where Kh will be)
       if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
-      if (tid == 96) {
+      if (warp == 3 && elect_one()) {
         tc::fence_after_sync();
         for (int b = 0; b < nb; ++b)
 #pragma unroll
@@ -465,14 +477,14 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         tc::fence_before_sync();
         if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
         // Two threads issue: it takes one about 70 cycles per product.
-        if (tid == 32) {
+        if (warp == 1 && elect_one()) {
           tc::fence_after_sync();
 #pragma unroll
           for (int s = 0; s < kD / 8; ++s)
             mma_tf32_ss(tmem + C::D2 + C::TH * hf, step_desc(x_desc, C::XR, s),
                         step_desc(kh_desc, TP, s), idesc_tf32(128, C::TH * (hf + 1)), s > 0);
           tc::mma_commit(bar_at(kMmaA));
-        } else if (tid == 64) {
+        } else if (warp == 2 && elect_one()) {
           tc::fence_after_sync();
 #pragma unroll
           for (int s = 0; s < kD / 8; ++s)
