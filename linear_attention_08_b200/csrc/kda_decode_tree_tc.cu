@@ -23,7 +23,9 @@
 // this one is computed.  A producer warp runs ahead: it finds the sets of ancestors and
 // brings the rows of tokens that are there; those of empty places are filled with zeros.
 //
-// The kernel is persistent.  TP = 16: two CTAs of 128 + 32 threads per SM, so that one
+// One CTA per unit is launched, and a CTA that runs takes over those that have not
+// started (launch control): units of ragged trees differ in cost by a factor of two.
+// TP = 16: two CTAs of 128 + 32 threads per SM, so that one
 // computes while the other waits for a product.  TP = 32, 64: the buffers allow one CTA,
 // of 256 + 32 threads; X holds 32 tokens at a time.
 #include "kda_common.cuh"
@@ -62,12 +64,14 @@ template <int TP> struct TreeTc {
   static constexpr uint32_t ALL = ANC + 2 * TP * 8;      // sets of tokens,
   static constexpr uint32_t PAR = ALL + 2 * 8;           // predecessors
   static constexpr uint32_t BETA = PAR + 2 * TP * 4;     // and beta
-  static constexpr uint32_t WIDE = BETA + 2 * TP * 4;
+  static constexpr uint32_t NEXT = BETA + 2 * TP * 4;    // answer of the launch control
+  static constexpr uint32_t ROW = NEXT + 16;             // two units' first rows, -1 at the end
+  static constexpr uint32_t WIDE = ROW + 16;
   static constexpr uint32_t QUIT = WIDE + 8;
   static constexpr uint32_t SLOT = QUIT + 4;
   static constexpr uint32_t BAR = SLOT + 4;
-  static constexpr uint32_t TOTAL = BAR + 11 * 8;
-  static_assert(X % 1024 == 0 && KH % 1024 == 0 && BETA % 16 == 0 && BAR % 8 == 0, "alignment");
+  static constexpr uint32_t TOTAL = BAR + 12 * 8;
+  static_assert(X % 1024 == 0 && KH % 1024 == 0 && NEXT % 16 == 0 && BAR % 8 == 0, "alignment");
   static_assert(ROWS * 128 * ((TP + 31) / 32) <= TP * kD * 4, "[KK; P] in Kh's place");
   static_assert(TP * 128 * ((TP + 31) / 32) <= XR * kD * 4, "A in X's place");
   // the A operand of D2 reads 128 rows, those past X into lanes that nobody reads
@@ -84,7 +88,7 @@ template <int TP> struct TreeTc {
 };
 
 enum TreeBar {
-  kFullQkg, kFullV, kFullS, kEmptyQkg, kEmptyV, kEmptyS, kMmaG, kMmaA, kMmaB, kMmaU, kMmaO, kBars
+  kFullQkg, kFullV, kFullS, kEmptyQkg, kEmptyV, kEmptyS, kMmaG, kMmaA, kMmaB, kMmaU, kMmaO, kNext, kBars
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
@@ -95,6 +99,30 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
 // An arrival once the calling thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Ask for a CTA of this grid that has not started; it then never does, and its work is
+// the caller's.  The answer is 16 bytes, announced on an mbarrier.
+__device__ __forceinline__ void ask_next(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          answer),
+      "r"(bar)
+      : "memory");
+}
+// Its number, or -1 when none is left (after which nothing more may be asked).
+__device__ __forceinline__ int read_next(uint32_t answer) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+      : "=&r"(r)
+      : "r"(answer)
+      : "memory");
+  return r;
 }
 
 // Instruction descriptor of kind::tf32, both operands K-major: as idesc_bf16 with
@@ -176,7 +204,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
                       const __nv_bfloat16 *__restrict__ v, const float *__restrict__ g,
                       const float *__restrict__ beta, const float *__restrict__ state,
                       const int32_t *__restrict__ parents, __nv_bfloat16 *__restrict__ out, int T,
-                      int H, int64_t units, int32_t *dev_status, uint64_t wait_ns) {
+                      int H, int32_t *dev_status, uint64_t wait_ns) {
   using C = TreeTc<TP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sraw = smem_u32(smem_raw);
@@ -187,7 +215,6 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
   volatile int *s_wide = reinterpret_cast<int *>(sp + C::WIDE);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be uniform
-  const int64_t G = gridDim.x;
   const auto bar_at = [&](int b) { return sb + C::BAR + 8 * b; };
 
   if (tid == 0) {
@@ -222,15 +249,26 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       }
     };
     constexpr int E = TP > 32 ? 2 : 1;    // places per lane
-    int64_t u = blockIdx.x;
+    volatile int64_t *s_row = reinterpret_cast<int64_t *>(sp + C::ROW);
+    int u = blockIdx.x;
     uint32_t states = 0;                  // copies of states begun
-    if (u < units) {
-      load_state(u);
-      states = 1;
-    }
-    for (uint32_t i = 0; u < units; u += G, ++i) {
-      const int n = (int)(u / H), h = (int)(u % H);
+    int asked = -1;                       // phase of an answer to come
+    bool ended = false;
+    for (uint32_t i = 0;; ++i) {
+      // the state's buffer is free once the unit before has it in tensor memory (and the
+      // one before that, which had this set of masks, is done)
+      const int buf = i & 1;
+      if (i > 0 && !wait(kEmptyS, (i - 1) & 1)) break;
+      const int n = u / H, h = u % H;
       const int64_t row0 = (int64_t)n * T * H + h;
+      if (lane == 0) s_row[buf] = row0;
+      load_state(u);
+      states = i + 1;
+      if (lane == 0) {
+        mbar_expect_tx(bar_at(kNext), 16);
+        ask_next(sb + C::NEXT, bar_at(kNext));
+      }
+      asked = i & 1;
       // ancestors by pointer doubling: after the step of size d every mask holds the
       // last 2 d places of its path
       int up[E], jump[E];
@@ -279,10 +317,8 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         all |= (unsigned long long)__ballot_sync(0xffffffffu, live[e]) << (32 * e);
       }
       const int rows = all ? (64 - __clzll(all) + kBlk - 1) / kBlk * kBlk : 0;
-      // the rows' buffers: free once the unit before has formed its operands (the one
-      // before that, which had this set of masks, is then done)
+      // the rows' buffers: free once the unit before has formed its operands
       if (i > 0 && !wait(kEmptyQkg, (i - 1) & 1)) break;
-      const int buf = i & 1;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int t = lane + 32 * e;
@@ -307,12 +343,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         cp_async16(dkq + t * 256, kq + at, there);
       }
       cp_async_arrive(bar_at(kFullQkg));
-      if (i > 0) {
-        if (!wait(kEmptyS, (i - 1) & 1)) break;
-        load_state(u);
-        states = i + 1;
-        if (!wait(kEmptyV, (i - 1) & 1)) break;
-      }
+      if (i > 0 && !wait(kEmptyV, (i - 1) & 1)) break;
       if (lane == 0) mbar_arrive(bars + kFullV);
 #pragma unroll 4
       for (int t0 = 0; t0 < rows; t0 += 2) {   // two rows at once
@@ -322,10 +353,25 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         cp_async16(sb + C::RV + t * 256 + 16 * (lane & 15), v + at + 8 * (lane & 15), there);
       }
       cp_async_arrive(bar_at(kFullV));
+      // the next unit, asked for a unit ago
+      if (!wait(kNext, i & 1)) break;
+      asked = -1;
+      u = read_next(sb + C::NEXT);
+      tc::fence_smem_to_async();          // read before it is written again
+      __syncwarp();
+      if (u < 0) {
+        ended = wait(kEmptyS, i & 1);   // (so this unit's state has arrived)
+        if (ended && lane == 0) {
+          s_row[buf ^ 1] = -1;
+          mbar_arrive(bars + kFullS);
+        }
+        break;
+      }
     }
     // copies in flight end before the memory is released
     cp_async_wait_all();
-    if (states) wait_timed(bars + kFullS, (states - 1) & 1, wait_ns);
+    if (!ended) wait_timed(bars + kFullS, (states - 1) & 1, wait_ns);
+    if (asked >= 0) wait_timed(bars + kNext, (uint32_t)asked, wait_ns);
   } else {
     // ------------------------------------------------------------ computing threads
     const int hw = warp >> 2;                        // warpgroup
@@ -375,16 +421,19 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       }
     };
     uint32_t i = 0;
-    for (int64_t u = blockIdx.x; u < units; u += G, ++i) {
+    for (;; ++i) {
       const uint32_t ph = i & 1;
-      const int n = (int)(u / H), h = (int)(u % H);
-      const int64_t row0 = (int64_t)n * T * H + h;
       const unsigned long long *s_anc = reinterpret_cast<unsigned long long *>(sp + C::ANC) + ph * TP;
       const int *s_par = reinterpret_cast<int *>(sp + C::PAR) + ph * TP;
       const float *s_beta = reinterpret_cast<float *>(sp + C::BETA) + ph * TP;
 
       // ---- S0^T into tensor memory ----
       bad |= !wait_timed(bars + kFullS, ph, wait_ns);
+      const int64_t row0 = *reinterpret_cast<volatile int64_t *>(sp + C::ROW + 8 * ph);
+      if (!bad && row0 < 0) {
+        bar_or<C::WORKERS>(false);         // a thread whose wait has run out is at its next barrier
+        break;
+      }
       {
         const float *sf = reinterpret_cast<const float *>(sp + C::SF) + col;
 #pragma unroll
@@ -402,7 +451,8 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       // ---- Gam along the paths: g (a thread per channel) and A ----
       bad |= !wait_timed(bars + kFullQkg, ph, wait_ns);
       const unsigned long long all = *reinterpret_cast<volatile unsigned long long *>(sp + C::ALL + 8 * ph);
-      const int nb = all ? (64 - __clzll(all) + kBlk - 1) / kBlk : 0;   // blocks up to the last token
+      const int last = all ? 64 - __clzll(all) : 0;                     // places up to the last token,
+      const int nb = (last + kBlk - 1) / kBlk;                          // blocks
       const int nh = (nb * kBlk + C::TH - 1) / C::TH;                   // and parts
       for (int b = hw; b < nb && b < TP / kBlk; b += C::WG) {
         float x[kBlk], y[kBlk];
@@ -461,6 +511,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           uint8_t *kt = sp + C::KH + (col >> 5) * TP * 128 + t0 * 128 + (col & 3) * 4;
 #pragma unroll
           for (int j = 0; j < kBlk; ++j) {
+            if (j == kBlk / 2 && t0 + j >= last) break;   // (what the rows held is masked)
             const float kv = __bfloat162float(rk[(t0 + j) * kD]), qv = __bfloat162float(rq[(t0 + j) * kD]);
             const float e = Gt[j] * 1.44269504f;     // to a power of two
             const float down = exp2_approx(e), d = kv * exp2_approx(-e);
@@ -588,7 +639,10 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           const uint8_t *kp = sp + C::KP + (TP > 32 ? (b >> 1) * C::ROWS * 128 : 0) + r0 * 128;
           const uint32_t flip = TP > kBlk ? (b & 1) * 64 : 0;   // column chunks 4 .. 7 of a row
 #pragma unroll
+          for (int j = kBlk / 2; j < kBlk; ++j) x[j] = 0.f;
+#pragma unroll
           for (int j = 0; j < kBlk; ++j) {
+            if (j == kBlk / 2 && kBlk * b + j >= last) break;
             float a = __bfloat162float(rv[(kBlk * b + j) * kD]) - ks[j];
 #pragma unroll
             for (int s4 = 0; s4 < j; s4 += 4) {
@@ -668,15 +722,9 @@ cudaError_t launch_tp(const void *q, const void *k, const void *v, const float *
   e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                            (int)cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 148;
-  // CTAs never wait on one another: a grid larger than what is resident is still correct.
-  const int64_t slots = (int64_t)(TP == 16 ? 2 : 1) * sms;
-  kern<<<(unsigned)(units < slots ? units : slots), C::THREADS, smem, stream>>>(
+  kern<<<(unsigned)units, C::THREADS, smem, stream>>>(
       (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k, (const __nv_bfloat16 *)v, g, beta, state,
-      parents, (__nv_bfloat16 *)out, T, H, units, dev_status, 2000000000ull);
+      parents, (__nv_bfloat16 *)out, T, H, dev_status, 2000000000ull);
   return cudaGetLastError();
 }
 
