@@ -7,18 +7,24 @@
 //
 //   token x at place i is accepted when r(x) > 0 and u_i R d_c(x) < r(x)
 //   accepted: c = i, r = p_i, R = 1
-//   refused:  r = max(r / R - d_c, 0), R = sum(r)
+//   refused:  r = max(r - R d_c, 0), R = sum(r)
 //
 // and when no successor is left the next token is the smallest j with
-// r(0) + ... + r(j) > u_last sum(r).  Accepted and drawn tokens then follow the
+// r(0) + ... + r(j) > u_last sum(r).  (r / R is what is left of the target's
+// distribution; the test and the draw do not change when r and R are scaled
+// together, so r is not divided by R, and may double with every refusal:
+// a + |a| = 2 max(a, 0) is one FP64 addition, a maximum four instructions.)  Accepted and drawn tokens then follow the
 // target's distribution exactly, for one drafted token per context (a chain)
 // and for several drawn from d_c (a tree).  Without a draft distribution (tokens
 // from a lookup, not a sample) d_c is one at the token itself: a refusal sets
 // r(x) = 0 and takes p_c(x) from R.
 //
-// Sums, quotients and comparisons are FP64: a token's border in the cumulative
-// sum has to come out the same whatever order the sum is taken in, and FP32
-// would move one draw in some hundreds at 10^5 tokens.
+// Sums and comparisons are FP64: a token's border in the cumulative sum has to come
+// out the same whatever order the sum is taken in, and FP32 would move one draw in
+// some hundreds at 10^5 tokens.  The probabilities' bits, shifted into place, are
+// their values times 2^-896 in FP64; the conversion instruction has a quarter of the
+// rate of the FP64 additions and was the bound (passes over 48 x 50256 FP32
+// elements after a refusal: 7 to 13 us before, 5 to 8 us now).
 //
 // Work: all successors' p and d are gathered at once, so a path of accepted
 // tokens reads no rows; only the last context's rows (and those of a context
@@ -41,78 +47,90 @@ constexpr int kVWarps = kVThreads / 32;
 constexpr int kVMaxNodes = 64;
 constexpr int kVMaxCluster = 8;
 
-template <typename P> struct VecOf;
-template <> struct VecOf<float> { static constexpr int N = 4; };
-template <> struct VecOf<__nv_bfloat16> { static constexpr int N = 8; };
+// Elements of one 16-byte load.
+template <typename P> constexpr int kVec = 16 / (int)sizeof(P);
 
-template <typename P> __device__ __forceinline__ void unpack16(uint4 x, float *f);
-template <> __device__ __forceinline__ void unpack16<float>(uint4 x, float *f) {
-  f[0] = __uint_as_float(x.x); f[1] = __uint_as_float(x.y);
-  f[2] = __uint_as_float(x.z); f[3] = __uint_as_float(x.w);
+// x times 2^-896, exactly, for x >= 0: an FP32 number's exponent and fraction in the
+// FP64 fields, subnormal ones too.  Whatever is not positive counts as zero.
+constexpr double kUnscale = 0x1p896;
+__device__ __forceinline__ double scaled(float x) {
+  const uint32_t b = __float_as_uint(fmaxf(x, 0.f));
+  return __hiloint2double((int)(b >> 3), (int)(b << 29));
 }
-template <> __device__ __forceinline__ void unpack16<__nv_bfloat16>(uint4 x, float *f) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ double scaled_bf16(uint32_t bits) {   // of the upper half
+  return __hiloint2double((int)(__float_as_uint(fmaxf(__uint_as_float(bits), 0.f)) >> 3), 0);
 }
 
-// What is left of a context's target distribution after its refusals, by case:
-// kWhole: none; kMinus: one, max(p - d, 0); kMany: several with a draft;
-// kGone: without a draft, the refused tokens' elements are zero.
-enum Mode { kWhole, kMinus, kMany, kGone };
-struct Rest {
-  bool draft;             // refusals subtract the draft's row (else zero a token)
-  int m;                  // refusals so far
-  const double *inv;      // 1 / R before each of them (1 before the first)
-  const int32_t *gone;    // the refused tokens
-  __device__ __forceinline__ Mode mode() const {
-    return m == 0 ? kWhole : !draft ? kGone : m == 1 ? kMinus : kMany;
-  }
-  // r of W neighbouring elements from `at` on.
-  template <int MODE, int W>
-  __device__ __forceinline__ void of(const float (&p)[W], const float (&d)[W], int at,
-                                     double (&r)[W]) const {
-#pragma unroll
-    for (int e = 0; e < W; ++e) r[e] = (double)p[e];
-    if (MODE == kMinus) {
-#pragma unroll
-      for (int e = 0; e < W; ++e) r[e] = p[e] > d[e] ? r[e] - (double)d[e] : 0.0;
-    } else if (MODE == kMany) {
-#pragma unroll 1
-      for (int l = 0; l < m; ++l) {
-        const double x = inv[l];
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          r[e] = r[e] * x - (double)d[e];
-          r[e] = r[e] > 0.0 ? r[e] : 0.0;
-        }
-      }
-    } else if (MODE == kGone) {
-#pragma unroll 1
-      for (int l = 0; l < m; ++l) {
-        const int x = gone[l] - at;
-#pragma unroll
-        for (int e = 0; e < W; ++e) r[e] = x == e ? 0.0 : r[e];
-      }
-    }
+// W neighbouring elements as one load gives them (one, or 16 bytes), and their values.
+template <typename P, int W> struct Raw;
+template <> struct Raw<float, 4> {
+  uint4 x;
+  __device__ __forceinline__ void load(const float *p) { x = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(double (&f)[4]) const {
+    f[0] = scaled(__uint_as_float(x.x)); f[1] = scaled(__uint_as_float(x.y));
+    f[2] = scaled(__uint_as_float(x.z)); f[3] = scaled(__uint_as_float(x.w));
   }
 };
-
-// W neighbouring elements as one load gives them (one, or 16 bytes), and as floats.
-template <typename P, int W> struct Raw {
+template <> struct Raw<__nv_bfloat16, 8> {
   uint4 x;
-  __device__ __forceinline__ void load(const P *p) { x = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    x = __ldg(reinterpret_cast<const uint4 *>(p));
+  }
   __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&f)[W]) const { unpack16<P>(x, f); }
+  __device__ __forceinline__ void get(double (&f)[8]) const {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = scaled_bf16(w[i] << 16);
+      f[2 * i + 1] = scaled_bf16(w[i] & 0xffff0000u);
+    }
+  }
 };
 template <typename P> struct Raw<P, 1> {
   P x;
   __device__ __forceinline__ void load(const P *p) { x = __ldg(p); }
   __device__ __forceinline__ void clear() { x = from_f32<P>(0.f); }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(x); }
+  __device__ __forceinline__ void get(double (&f)[1]) const { f[0] = scaled(to_f32(x)); }
+};
+
+// What is left of a context's target distribution after its refusals, by case:
+// kWhole: none; kMinus: one, 2 max(p - d, 0); kMany: several with a draft;
+// kGone: without a draft, the refused tokens' elements are zero.
+enum Mode { kWhole, kMinus, kMany, kGone };
+struct Rest {
+  bool draft;             // refusals subtract the draft's row (else zero a token)
+  int m;                  // refusals so far
+  const double *sum;      // R before each of them (1 before the first)
+  const int32_t *gone;    // the refused tokens
+  __device__ __forceinline__ Mode mode() const {
+    return m == 0 ? kWhole : !draft ? kGone : m == 1 ? kMinus : kMany;
+  }
+  // r of B times W neighbouring elements, those of one b from `at` + b `step` on, from p
+  // and d; all times 2^-896.
+  template <int MODE, int B, int W>
+  __device__ __forceinline__ void of(double (&r)[B][W], const double (&d)[B][W], int at,
+                                     int step) const {
+    if (MODE == kWhole) return;
+    const int n = MODE == kMinus ? 1 : m;
+#pragma unroll 1
+    for (int l = 0; l < n; ++l) {
+      const double R = MODE == kMany ? -sum[l] : -1.0;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int x = MODE == kGone ? gone[l] - (at + b * step) : 0;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          if (MODE == kGone) {
+            r[b][e] = x == e ? 0.0 : r[b][e];
+          } else {
+            r[b][e] = MODE == kMany ? fma(R, d[b][e], r[b][e]) : r[b][e] - d[b][e];
+            r[b][e] += fabs(r[b][e]);
+          }
+        }
+      }
+    }
+  }
 };
 
 // Sum of the rest over [lo, hi) over the calling lanes' strided loads of W
@@ -120,35 +138,44 @@ template <typename P> struct Raw<P, 1> {
 template <typename P, int MODE, int W>
 __device__ __forceinline__ double sum_w(const P *p, const P *d, const Rest &rest, int lo, int hi,
                                         int lane) {
-  constexpr int B = MODE == kMany ? 1 : W == 1 ? 8 : 4;
+  constexpr int B = W == 1 ? 8 : 4, G = 8 / W;
   constexpr bool D = MODE == kMinus || MODE == kMany;
   double acc = 0.0;
 #pragma unroll 1
   for (int i = lo + lane * W; i < hi; i += B * 32 * W) {
-    Raw<P, W> a[B], b[B];
+    Raw<P, W> p0[B], d0[B];
 #pragma unroll
     for (int j = 0; j < B; ++j) {
       const int at = i + j * 32 * W;
       if (at < hi) {
-        a[j].load(p + at);
-        if (D) b[j].load(d + at);
+        p0[j].load(p + at);
+        if (D) d0[j].load(d + at);
       } else {
-        a[j].clear();
-        if (D) b[j].clear();
+        p0[j].clear();
+        if (D) d0[j].clear();
       }
     }
 #pragma unroll
-    for (int j = 0; j < B; ++j) {
-      float x[W], y[W];
-      double r[W];
-      a[j].get(x);
-      if (D) b[j].get(y);
-      rest.of<MODE, W>(x, y, i + j * 32 * W, r);
+    for (int j = 0; j < B; j += G) {       // G loads' elements at once
+      double r[G][W], y[G][W];
 #pragma unroll
-      for (int o = 1; o < W; o <<= 1)      // pairs first: short chains of FP64 additions
+      for (int b = 0; b < G; ++b) {
+        p0[j + b].get(r[b]);
+        if (D) d0[j + b].get(y[b]);
+      }
+      rest.of<MODE, G, W>(r, y, i + j * 32 * W, 32 * W);
 #pragma unroll
-        for (int e = 0; e + o < W; e += 2 * o) r[e] += r[e + o];
-      acc += r[0];
+      for (int b = 0; b < G; ++b) {
+#pragma unroll
+        for (int o = 1; o < W; o <<= 1)    // pairs first: short chains of FP64 additions
+#pragma unroll
+          for (int e = 0; e + o < W; e += 2 * o) r[b][e] += r[b][e + o];
+      }
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1)
+#pragma unroll
+        for (int b = 0; b + o < G; b += 2 * o) r[b][0] += r[b + o][0];
+      acc += r[0][0];
     }
   }
   return acc;
@@ -159,7 +186,7 @@ __device__ __forceinline__ double sum_w(const P *p, const P *d, const Rest &rest
 template <typename P, int MODE>
 __device__ __noinline__ double sum_mode(const P *p, const P *d, const Rest &rest, int lo, int hi,
                                         int lane) {
-  constexpr int V = VecOf<P>::N;
+  constexpr int V = kVec<P>;
   constexpr bool D = MODE == kMinus || MODE == kMany;
   uintptr_t bits = reinterpret_cast<uintptr_t>(p + lo);
   if (D) bits |= reinterpret_cast<uintptr_t>(d + lo);
@@ -179,13 +206,13 @@ __device__ __forceinline__ double rest_sum(const P *p, const P *d, const Rest &r
     default: return sum_mode<P, kGone>(p, d, rest, lo, hi, lane);
   }
 }
-// One element's.
+// One element's, unscaled.
 __device__ __forceinline__ double rest_one(const Rest &rest, float p, float d, int at) {
-  const float a[1] = {p}, b[1] = {d};
-  double r[1];
-  if (rest.draft) rest.of<kMany, 1>(a, b, at, r);
-  else rest.of<kGone, 1>(a, b, at, r);
-  return r[0];
+  double r[1][1] = {{scaled(p)}};
+  const double y[1][1] = {{scaled(d)}};
+  if (rest.draft) rest.of<kMany, 1, 1>(r, y, at, 0);
+  else rest.of<kGone, 1, 1>(r, y, at, 0);
+  return r[0][0] * kUnscale;
 }
 
 template <typename P>
@@ -198,7 +225,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   __shared__ int32_t s_tok[kVMaxNodes], s_par[kVMaxNodes], s_path[kVMaxNodes], s_gone[kVMaxNodes];
   __shared__ float s_u[kVMaxNodes + 1];
   __shared__ float s_p[kVMaxNodes], s_d[kVMaxNodes];
-  __shared__ double s_inv[kVMaxNodes];
+  __shared__ double s_sum[kVMaxNodes];
   __shared__ double s_warp[kVWarps], s_scan[kVWarps];
   __shared__ double s_tot[2][kVMaxCluster];   // the CTAs' sums, one buffer per parity of the pass
   __shared__ int s_last[kVWarps];
@@ -212,7 +239,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   const P *drow = draft ? draft + n * T * (int64_t)vocab : nullptr;
 
   // Slices of whole 16-byte vectors: CTA, then warp.
-  constexpr int V = VecOf<P>::N;
+  constexpr int V = kVec<P>;
   const int piece = ((vocab + CS * kVWarps - 1) / (CS * kVWarps) + V - 1) / V * V;
   const auto bound = [&](int w) {   // start of warp slice w of the whole cluster
     const int64_t b = (int64_t)w * piece;
@@ -234,7 +261,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   if (CS > 1) cluster.barrier_wait();
 
   // Every thread of the cluster takes the same decisions from here on.
-  Rest rest{drow != nullptr, 0, s_inv, s_gone};
+  Rest rest{drow != nullptr, 0, s_sum, s_gone};
   int cur = -1, count = 0, pass = 0;
   double R = 1.0;
   // Sums of the rest over warps, CTAs and the cluster.
@@ -242,17 +269,21 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     const int w = rank * kVWarps + warp;
     double x = rest_sum<P>(trow + (int64_t)(cur + 1) * vocab,
                            rest.draft ? drow + (int64_t)min(cur + 1, T - 1) * vocab : nullptr, rest,
-                           bound(w), bound(w + 1), lane);
+                           bound(w), bound(w + 1), lane) * kUnscale;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lane == 0) s_warp[warp] = x;
     __syncthreads();
     const int buf = pass++ & 1;
     if (tid < CS) {
-      double t = 0.0;
+      double t[kVWarps];
 #pragma unroll
-      for (int i = 0; i < kVWarps; ++i) t += s_warp[i];
-      cluster.map_shared_rank(&s_tot[buf][0], tid)[rank] = t;
+      for (int i = 0; i < kVWarps; ++i) t[i] = s_warp[i];
+#pragma unroll
+      for (int o = 1; o < kVWarps; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < kVWarps; i += 2 * o) t[i] += t[i + o];
+      cluster.map_shared_rank(&s_tot[buf][0], tid)[rank] = t[0];
     }
     if (CS > 1) cluster.sync();
     else __syncthreads();
@@ -274,7 +305,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     } else {
       __syncthreads();   // the rest's lists are read by every thread
       if (tid == 0) {
-        s_inv[rest.m] = R > 0.0 ? 1.0 / R : 1.0;
+        s_sum[rest.m] = R;
         s_gone[rest.m] = s_tok[i];
       }
       if (!rest.draft) R -= r;
@@ -379,11 +410,12 @@ cudaError_t launch_verify_tree(bool bf16, const void *target, const void *draft,
                                const float *uniforms, int32_t *accept_node, int32_t *accept_len,
                                int32_t *out_tokens, int N, int T, int vocab, int num_sms,
                                cudaStream_t stream) {
-  // CTAs per sequence: as many as keep the grid within the two CTAs that an SM
-  // holds (a lone sequence is bound by what its few SMs can load) and leave each a
-  // 16-byte load per thread, at most the portable cluster size.
+  // CTAs per sequence: as many as keep the grid within the two CTAs that an SM holds
+  // (a lone sequence is bound by what its few SMs can load) and leave each a 16-byte
+  // load per thread, at most the portable cluster size.  Twice as many: 64 chains of
+  // 131072 elements 21 us instead of 15, 48 trees of 50257 elements no different.
   int cs = kVMaxCluster;
-  const int least = kVThreads * (bf16 ? VecOf<__nv_bfloat16>::N : VecOf<float>::N);
+  const int least = kVThreads * (bf16 ? kVec<__nv_bfloat16> : kVec<float>);
   while (cs > 1 && ((int64_t)N * cs > 2 * (int64_t)num_sms || vocab <= (cs / 2) * least)) cs >>= 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)N * cs));
