@@ -8,127 +8,203 @@
 //
 // The state crosses HBM once in each direction however long the path is, which
 // is what bounds the kernel: 128 KB per (sequence, head) at D = 128 against
-// 3 D^2 FP32 operations per token, so about twelve tokens hide behind the
-// traffic.  Columns of S do not mix, so a warp owns 16 whole columns: its lanes
-// are 4 float4 column groups x 8 row residues, the reduction over rows stays
-// inside the warp, and the warps run the whole path without a block barrier
-// except where the next group of tokens is staged.
+// 3 D^2 FP32 operations per token.  Columns of S do not mix, so a CTA takes up to
+// 64 columns of a unit, a warp 16 of them: its lanes are 4 float4 column groups x 8
+// row residues, and the reduction over rows stays inside the warp.
+//
+// CTAs are persistent and work on the next unit's loads while they compute: every
+// thread copies the elements it will hold into shared memory (its own slots, no
+// barrier), takes them into registers when the unit begins, and starts the next
+// unit's copies into the same slots.  accept_node and parents are read two units
+// ahead, the path's first rows one unit ahead.  (Without this a CTA waited in turn
+// for accept_node, the state and the rows: 512 x 32 units in 416 us; 366 with it, 91 %
+// of the copy rate.)
 #include "kda_common.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kGroup = 8;        // tokens staged at a time
+constexpr int kGroup = 4;        // tokens staged at a time
 
-// Value columns of one CTA.
-template <int DV> constexpr int kCols = DV < 64 ? DV : 64;
+template <int DK, int DV, typename TIn> struct CommitCfg {
+  static constexpr int COLS = DV < 64 ? DV : 64, PARTS = DV / COLS;   // value columns of a CTA
+  static constexpr int THREADS = 2 * COLS;      // 16 columns per warp
+  static constexpr int ROWS = DK / 8;           // float4s per thread
+  // 16-byte pieces of one token's g, k, v
+  static constexpr int CG = DK / 4, CK = DK * (int)sizeof(TIn) / 16, CV = COLS * (int)sizeof(TIn) / 16;
+  static constexpr int CT = CG + CK + CV;
+  static constexpr int SMEM = DK * COLS * 4 + kGroup * (DK * 8 + COLS * 4 + CT * 16 + 8);
+  static constexpr int FIT = 227 * 1024 / (SMEM + 1024);
+  static constexpr int PER_SM = FIT < 8 ? FIT : 8;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Place of the j-th token of a path, from the state on (a token's place is above its
+// predecessor's).
+__device__ __forceinline__ int nth(unsigned long long path, int j) {
+  for (; j > 0; --j) path &= path - 1;
+  return __ffsll(path) - 1;
+}
 
 template <int DK, int DV, typename TIn>
-__global__ void __launch_bounds__(2 * kCols<DV>, 640 / (2 * kCols<DV>))
+__global__ void __launch_bounds__(CommitCfg<DK, DV, TIn>::THREADS, CommitCfg<DK, DV, TIn>::PER_SM)
 tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
                    const float *__restrict__ g, const float *__restrict__ beta,
                    const float *state, float *state_out, const int32_t *__restrict__ parents,
-                   const int32_t *__restrict__ accept_node, int T, int H) {
-  constexpr int COLS = kCols<DV>, PARTS = DV / COLS;
-  constexpr int THREADS = 2 * COLS;           // 16 columns per warp
+                   const int32_t *__restrict__ accept_node, int T, int H, int64_t items) {
+  using C = CommitCfg<DK, DV, TIn>;
+  constexpr int COLS = C::COLS, PARTS = C::PARTS, THREADS = C::THREADS, ROWS = C::ROWS;
   constexpr int V4 = DV / 4;
-  constexpr int ROWS = DK / 8;                // float4s per thread
+  __shared__ float4 s_state[ROWS][THREADS];   // the next unit's elements
+  __shared__ uint4 s_raw[kGroup][C::CT];      // its path's first rows: g, k, v
+  __shared__ float s_rb[kGroup];              // and beta
   __shared__ float2 s_ak[kGroup][DK];         // (alpha, k)
   __shared__ float s_v[kGroup][COLS];
   __shared__ float s_b[kGroup];
 
-  const int64_t unit = blockIdx.x / PARTS;
-  const int part = blockIdx.x % PARTS;
-  const int n = (int)(unit / H), h = (int)(unit % H);
   const int tid = threadIdx.x, lane = tid & 31;
   const int cg = 4 * (tid >> 5) + (lane & 3);  // float4 column
   const int ks = lane >> 2;                    // rows ks, ks + 8, ...
+  const bool in_place = state_out == state;
+  const int64_t G = gridDim.x;
 
-  const int32_t node = __ldg(accept_node + n);
-  int32_t up0 = -2, up1 = -2;                  // predecessors of places lane and lane + 32
-  if (parents) {
-    if (lane < T) up0 = __ldg(parents + (int64_t)n * T + lane);
-    if (lane + 32 < T) up1 = __ldg(parents + (int64_t)n * T + lane + 32);
-  }
-  // In place, a sequence without an accepted token is not touched; otherwise the
-  // state is loaded before anything is known of the path.
-  const bool named = node >= 0 && node < T;
-  if (state_out == state && !named) return;
-  const float4 *src = reinterpret_cast<const float4 *>(state) + unit * (DK * V4) + part * (COLS / 4);
-  float4 *dst = reinterpret_cast<float4 *>(state_out) + unit * (DK * V4) + part * (COLS / 4);
-  float4 s[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) s[i] = __ldcs(src + (ks + 8 * i) * V4 + cg);
-
-  // The path as a set of places (a token's place is above its predecessor's), found
-  // by every warp for itself: no shared memory, no barrier.
-  unsigned long long path = 0;
-  if (named && parents) {
+  // An item is the columns of one CTA: PARTS of them per unit.
+  int node = -1, up0 = -2, up1 = -2;           // predecessors of places lane and lane + 32
+  const auto read_ahead = [&](int64_t item) {
+    if (item >= items) return;
+    const int64_t n = item / PARTS / H;
+    node = __ldg(accept_node + n);
+    if (parents) {
+      if (lane < T) up0 = __ldg(parents + n * T + lane);
+      if (lane + 32 < T) up1 = __ldg(parents + n * T + lane + 32);
+    }
+  };
+  // The path as a set of places, found by every warp for itself.
+  const auto find_path = [&] {
+    unsigned long long path = 0;
+    if (node < 0 || node >= T) return path;
+    if (!parents) return ~0ull >> (63 - node);
     for (int i = node; i >= 0;) {              // at most T steps: i decreases
       path |= 1ull << i;
       const int up = __shfl_sync(0xffffffffu, i < 32 ? up0 : up1, i & 31);
-      if (up < -1 || up >= i) { path = 0; break; }   // it holds an empty place
+      if (up < -1 || up >= i) return 0ull;     // it holds an empty place
       i = up;
     }
-  } else if (named) {
-    path = ~0ull >> (63 - node);
-  }
-  if (state_out == state && path == 0) return;
-
-  const int64_t row0 = (int64_t)n * T * H + h;
-  for (bool first = true; path != 0; first = false) {
+    return path;
+  };
+  const auto elements = [&](int64_t item) {    // this thread's, in float4s
+    return item / PARTS * (DK * V4) + item % PARTS * (COLS / 4) + (int64_t)ks * V4 + cg;
+  };
+  const auto first_row = [&](int64_t item) {
+    const int64_t unit = item / PARTS;
+    return unit / H * T * H + unit % H;
+  };
+  const auto start_copies = [&](int64_t item, unsigned long long path) {
+    if (path == 0 && in_place) return;         // a state that is not touched
+    const float4 *src = reinterpret_cast<const float4 *>(state) + elements(item);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) copy16(smem_u32(&s_state[i][tid]), src + i * 8 * V4);
     const int m = min(kGroup, __popcll(path));
-    if (!first) __syncthreads();
-    const unsigned long long all = path;
-#pragma unroll
-    for (int e0 = 0; e0 < DK + COLS; e0 += THREADS) {
-      const int e = e0 + tid;
-      unsigned long long rest = all;
-#pragma unroll 4
-      for (int j = 0; j < kGroup; ++j) {
-        if (j < m && e < DK + COLS) {
-          const int64_t row = row0 + (int64_t)(__ffsll(rest) - 1) * H;
-          if (e < DK) s_ak[j][e] = make_float2(expf(g[row * DK + e]), to_f32(k[row * DK + e]));
-          else s_v[j][e - DK] = to_f32(v[row * DV + part * COLS + (e - DK)]);
-          if (e == 0) s_b[j] = beta[row];
-        }
-        rest &= rest - 1;
-      }
-      path = rest;
+    const int64_t row0 = first_row(item);
+    for (int e = tid; e < m * C::CT; e += THREADS) {
+      const int j = e / C::CT, c = e % C::CT;
+      const int64_t row = row0 + (int64_t)nth(path, j) * H;
+      const void *from = c < C::CG ? static_cast<const void *>(g + row * DK + c * 4)
+                         : c < C::CG + C::CK
+                             ? static_cast<const void *>(k + row * DK + (c - C::CG) * (16 / (int)sizeof(TIn)))
+                             : static_cast<const void *>(v + row * DV + item % PARTS * COLS +
+                                                         (c - C::CG - C::CK) * (16 / (int)sizeof(TIn)));
+      copy16(smem_u32(&s_raw[j][c]), from);
     }
+    if (tid < m) copy4(smem_u32(&s_rb[tid]), beta + row0 + (int64_t)nth(path, tid) * H);
+  };
+
+  int64_t item = blockIdx.x;
+  read_ahead(item);
+  unsigned long long path = find_path();
+  start_copies(item, path);
+  read_ahead(item + G);
+  for (; item < items; item += G) {
+    const int64_t next = item + G;
+    const unsigned long long next_path = next < items ? find_path() : 0ull;
+    read_ahead(next + G);
+    const bool active = path != 0 || !in_place;
+    float4 s[ROWS];
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                           // the others' copies of rows; the last unit's are used up
+    if (active) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) s[i] = s_state[i][tid];
+    }
+    int m = min(kGroup, __popcll(path));
+    for (int e = tid; e < m * DK; e += THREADS) {
+      const int j = e / DK, c = e % DK;
+      s_ak[j][c] = make_float2(expf(reinterpret_cast<const float *>(&s_raw[j][0])[c]),
+                               to_f32(reinterpret_cast<const TIn *>(&s_raw[j][C::CG])[c]));
+    }
+    for (int e = tid; e < m * COLS; e += THREADS)
+      s_v[e / COLS][e % COLS] = to_f32(reinterpret_cast<const TIn *>(&s_raw[e / COLS][C::CG + C::CK])[e % COLS]);
+    if (tid < m) s_b[tid] = s_rb[tid];
     __syncthreads();
-    for (int j = 0; j < m; ++j) {
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (next < items) start_copies(next, next_path);
+    if (active) {
+      while (m > 0) {
+        for (int j = 0; j < m; ++j) {
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const float2 ak = s_ak[j][ks + 8 * i];
-        s[i].x *= ak.x; s[i].y *= ak.x; s[i].z *= ak.x; s[i].w *= ak.x;
-        y.x += ak.y * s[i].x; y.y += ak.y * s[i].y; y.z += ak.y * s[i].z; y.w += ak.y * s[i].w;
-      }
-      // Sum over the 8 row residues: each step halves the columns a lane
-      // keeps, so a lane ends with one column (7 shuffles, not 12).
-      const bool b4 = lane & 16, b3 = lane & 8;
-      float p0 = b4 ? y.z : y.x, p1 = b4 ? y.w : y.y;
-      p0 += __shfl_xor_sync(0xffffffffu, b4 ? y.x : y.z, 16);
-      p1 += __shfl_xor_sync(0xffffffffu, b4 ? y.y : y.w, 16);
-      float w = b3 ? p1 : p0;
-      w += __shfl_xor_sync(0xffffffffu, b3 ? p0 : p1, 8);
-      w += __shfl_xor_sync(0xffffffffu, w, 4);
-      const float u = s_b[j] * (s_v[j][4 * cg + (b4 ? 2 : 0) + (b3 ? 1 : 0)] - w);
-      const float u8 = __shfl_xor_sync(0xffffffffu, u, 8);
-      const float ua = b3 ? u8 : u, ub = b3 ? u : u8;
-      const float ua16 = __shfl_xor_sync(0xffffffffu, ua, 16);
-      const float ub16 = __shfl_xor_sync(0xffffffffu, ub, 16);
-      const float4 u4 = b4 ? make_float4(ua16, ub16, ua, ub) : make_float4(ua, ub, ua16, ub16);
+          for (int i = 0; i < ROWS; ++i) {
+            const float2 ak = s_ak[j][ks + 8 * i];
+            s[i].x *= ak.x; s[i].y *= ak.x; s[i].z *= ak.x; s[i].w *= ak.x;
+            y.x += ak.y * s[i].x; y.y += ak.y * s[i].y; y.z += ak.y * s[i].z; y.w += ak.y * s[i].w;
+          }
+          // Sum over the 8 row residues: each step halves the columns a lane
+          // keeps, so a lane ends with one column (7 shuffles, not 12).
+          const bool b4 = lane & 16, b3 = lane & 8;
+          float p0 = b4 ? y.z : y.x, p1 = b4 ? y.w : y.y;
+          p0 += __shfl_xor_sync(0xffffffffu, b4 ? y.x : y.z, 16);
+          p1 += __shfl_xor_sync(0xffffffffu, b4 ? y.y : y.w, 16);
+          float w = b3 ? p1 : p0;
+          w += __shfl_xor_sync(0xffffffffu, b3 ? p0 : p1, 8);
+          w += __shfl_xor_sync(0xffffffffu, w, 4);
+          const float u = s_b[j] * (s_v[j][4 * cg + (b4 ? 2 : 0) + (b3 ? 1 : 0)] - w);
+          const float u8 = __shfl_xor_sync(0xffffffffu, u, 8);
+          const float ua = b3 ? u8 : u, ub = b3 ? u : u8;
+          const float ua16 = __shfl_xor_sync(0xffffffffu, ua, 16);
+          const float ub16 = __shfl_xor_sync(0xffffffffu, ub, 16);
+          const float4 u4 = b4 ? make_float4(ua16, ub16, ua, ub) : make_float4(ua, ub, ua16, ub16);
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const float kc = s_ak[j][ks + 8 * i].y;
-        s[i].x += kc * u4.x; s[i].y += kc * u4.y; s[i].z += kc * u4.z; s[i].w += kc * u4.w;
+          for (int i = 0; i < ROWS; ++i) {
+            const float kc = s_ak[j][ks + 8 * i].y;
+            s[i].x += kc * u4.x; s[i].y += kc * u4.y; s[i].z += kc * u4.z; s[i].w += kc * u4.w;
+          }
+        }
+        // the path's further tokens, read when they are needed
+        for (int j = 0; j < m; ++j) path &= path - 1;
+        m = min(kGroup, __popcll(path));
+        if (m == 0) break;
+        const int64_t row0 = first_row(item);
+        __syncthreads();
+        for (int e = tid; e < m * (DK + COLS); e += THREADS) {
+          const int j = e / (DK + COLS), c = e % (DK + COLS);
+          const int64_t row = row0 + (int64_t)nth(path, j) * H;
+          if (c < DK) s_ak[j][c] = make_float2(expf(g[row * DK + c]), to_f32(k[row * DK + c]));
+          else s_v[j][c - DK] = to_f32(v[row * DV + item % PARTS * COLS + (c - DK)]);
+          if (c == 0) s_b[j] = beta[row];
+        }
+        __syncthreads();
       }
+      float4 *dst = reinterpret_cast<float4 *>(state_out) + elements(item);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) __stcs(dst + i * 8 * V4, s[i]);
     }
+    path = next_path;
   }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) __stcs(dst + (ks + 8 * i) * V4 + cg, s[i]);
 }
 
 template <typename TIn>
@@ -136,11 +212,22 @@ cudaError_t launch_t(int dk, int dv, const void *k, const void *v, const float *
                      const float *beta, const float *state, float *state_out,
                      const int32_t *parents, const int32_t *accept_node, int T, int64_t units,
                      int H, cudaStream_t stream) {
-#define KDA_TC(DK_, DV_)                                                                         \
-  if (dk == DK_ && dv == DV_) {                                                                  \
-    tree_commit_kernel<DK_, DV_, TIn><<<(unsigned)(units * (DV_ / kCols<DV_>)), 2 * kCols<DV_>, 0, stream>>>( \
-        (const TIn *)k, (const TIn *)v, g, beta, state, state_out, parents, accept_node, T, H);  \
-    return cudaGetLastError();                                                                   \
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 148;
+#define KDA_TC(DK_, DV_)                                                                          \
+  if (dk == DK_ && dv == DV_) {                                                                   \
+    using C = CommitCfg<DK_, DV_, TIn>;                                                           \
+    const int64_t items = units * C::PARTS, slots = (int64_t)C::PER_SM * sms;                     \
+    const cudaError_t e = cudaFuncSetAttribute(tree_commit_kernel<DK_, DV_, TIn>,                 \
+                                               cudaFuncAttributePreferredSharedMemoryCarveout,    \
+                                               (int)cudaSharedmemCarveoutMaxShared);              \
+    if (e != cudaSuccess) return e;                                                               \
+    tree_commit_kernel<DK_, DV_, TIn><<<(unsigned)(items < slots ? items : slots), C::THREADS, 0, \
+                                        stream>>>((const TIn *)k, (const TIn *)v, g, beta, state, \
+                                                  state_out, parents, accept_node, T, H, items);  \
+    return cudaGetLastError();                                                                    \
   }
   KDA_TC(32, 32) KDA_TC(32, 64) KDA_TC(32, 128)
   KDA_TC(64, 32) KDA_TC(64, 64) KDA_TC(64, 128)
