@@ -1,4 +1,5 @@
-"""Build libkda.so (all CUDA sources, sm_100a) in-tree with nvcc.
+"""Build libkda.so (all CUDA sources, sm_100a) in-tree with nvcc, and _binding.so (the native part
+of the Python binding) with g++.
 
 Usage: python -m linear_attention_08_b200.build [--force]
 """
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+BINDING = os.path.join(PKG, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -29,11 +31,36 @@ def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "kda.h")]
 
 
+def _newer(out: str, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
+def _binding_deps():
+    return [os.path.join(CSRC, "kda_binding.cpp"), os.path.join(ROOT, "include", "kda.h")]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps()) and _newer(BINDING, _binding_deps())
+
+
+def _build_binding() -> None:
+    """_binding.so: the native part of the Python binding, over PyTorch's C++ headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    inc = include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(NVCC), "..", "include"),
+                             os.path.join(ROOT, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for p in inc for x in ("-isystem", p)), _binding_deps()[0], "-o", tmp,
+           *(f"-L{p}" for p in library_paths()), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           f"-L{PKG}", "-l:libkda.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding failed to compile:\n{res.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -52,12 +79,16 @@ def _compile(src: str, verbose: bool) -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
+    if not force and _newer(LIB, _deps()):
+        _build_binding()
+        return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), _sources()))
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
     os.replace(tmp, LIB)
+    _build_binding()
     return LIB
 
 

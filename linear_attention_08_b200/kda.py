@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libkda.so (the C ABI declared in include/kda.h).
+"""Thin binding of libkda.so (the C ABI declared in include/kda.h), by ctypes; the calls
+of speculative decoding and of the state cache by a native module (_binding.so).
 
 Argument marshalling only: every step of the operator runs in the CUDA
 kernels behind the C ABI.  PyTorch provides device memory and streams.  There
@@ -7,7 +8,6 @@ is no fallback: if the library is missing or a call fails, this module raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -351,58 +351,25 @@ def kda_decode_multi(q, k, v, g, beta, state, *, accept_len=None, out=None, dev_
     return out
 
 
-def _want(name, t, shape, dtype, device):
-    """Check one argument of the calls below: a dense CUDA tensor of this shape and dtype."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
-        return
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on one CUDA device with the other arguments, got {t.device}")
-    raise ValueError(f"{name} must be contiguous")
+_native_module = None
 
 
-# Shapes of the calls below, which only read them, by their sizes: building the
-# struct is a tenth of what the host spends on a call.
-_shape = functools.lru_cache(maxsize=1024)(make_shape)
+def _native():
+    """The native part of this binding (csrc/kda_binding.cpp): checks, outputs and the call."""
+    global _native_module
+    if _native_module is None:
+        load()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("_binding.so is missing or does not fit this PyTorch: build it with "
+                              f"`python -m linear_attention_08_b200.build` ({e})") from e
+        _native_module = _binding
+    return _native_module
 
 
-def _call(fn, device, stream, *args):
-    """Run a library call on the arguments' device and on ``stream`` (None: that
-    device's current stream).  Pointers are passed as integers and the device is
-    switched only when it is not the current one: small calls are bound by what the
-    host does before the launch."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-        st = getattr(_lib or load(), fn)(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            raw = (stream or torch.cuda.current_stream()).cuda_stream
-            st = getattr(load(), fn)(*args, raw)
-    if st != KDA_OK:
-        raise KdaError(st, fn)
-
-
-def _at(t):
-    """Address of an optional argument."""
-    return None if t is None else t.data_ptr()
-
-
-def _want_tree(k, v, g, beta, state, parents):
-    N, T, H, Dk = k.shape
-    Dv = v.shape[-1]
-    dev = k.device
-    _want("k", k, (N, T, H, Dk), k.dtype, dev)
-    _want("v", v, (N, T, H, Dv), k.dtype, dev)
-    _want("g", g, (N, T, H, Dk), torch.float32, dev)
-    _want("beta", beta, (N, T, H), torch.float32, dev)
-    _want("state", state, (N, H, Dk, Dv), torch.float32, dev)
-    if parents is not None:
-        _want("parents", parents, (N, T), torch.int32, dev)
-    return N, T, H, Dk, Dv
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def kda_decode_tree(q, k, v, g, beta, state, *, parents=None, out=None, stream=None):
@@ -410,17 +377,13 @@ def kda_decode_tree(q, k, v, g, beta, state, *, parents=None, out=None, stream=N
     kda_decode_tree in include/kda.h): q, k, g [N, T, H, Dk]; v [N, T, H, Dv];
     beta [N, T, H]; state [N, H, Dk, Dv] FP32, only read; parents [N, T] int32
     (place of the token before, -1 for the state, -2 for an empty place) or None
-    for chains; T <= 64.  Returns out [N, T, H, Dv], zero at empty places."""
-    N, T, H, Dk, Dv = _want_tree(k, v, g, beta, state, parents)
-    code = _dtype_code(k)
-    _want("q", q, k.shape, k.dtype, k.device)
-    if out is None:
-        out = torch.empty_like(v)
-    _want("out", out, v.shape, k.dtype, k.device)
-    shape = _shape(N, N * T, H, Dk, Dv, 0, code)
-    _call("kda_decode_tree", k.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          g.data_ptr(), beta.data_ptr(), state.data_ptr(), _at(parents), out.data_ptr(), T,
-          ctypes.byref(shape))
+    for chains; T <= 64.  Returns out [N, T, H, Dv], zero at empty places.
+
+    This call and the ones below run on the arguments' device, on ``stream`` or
+    that device's current stream."""
+    st, out = (_native_module or _native()).decode_tree(q, k, v, g, beta, state, parents, out, _raw(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_decode_tree")
     return out
 
 
@@ -430,16 +393,12 @@ def kda_tree_commit(k, v, g, beta, state, accept_node, *, parents=None, state_ou
     nothing) of each sequence's tree (see kda_tree_commit in include/kda.h),
     written to ``state_out``, or over ``state`` when it is None.  Other
     arguments as for kda_decode_tree.  Returns the tensor written."""
-    N, T, H, Dk, Dv = _want_tree(k, v, g, beta, state, parents)
-    code = _dtype_code(k)
-    _want("accept_node", accept_node, (N,), torch.int32, k.device)
     if state_out is None:
         state_out = state
-    _want("state_out", state_out, state.shape, torch.float32, k.device)
-    shape = _shape(N, N * T, H, Dk, Dv, 0, code)
-    _call("kda_tree_commit", k.device, stream, k.data_ptr(), v.data_ptr(), g.data_ptr(),
-          beta.data_ptr(), state.data_ptr(), state_out.data_ptr(), _at(parents),
-          accept_node.data_ptr(), T, ctypes.byref(shape))
+    st = (_native_module or _native()).tree_commit(k, v, g, beta, state, accept_node, parents, state_out,
+                                                   _raw(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_tree_commit")
     return state_out
 
 
@@ -453,44 +412,11 @@ def kda_verify_tree(target_probs, tokens, uniforms, *, draft_probs=None, parents
     the last accepted place (-1: none), the number of accepted tokens (the
     accept_len of kda_decode_multi), and the accepted tokens followed by the
     one drawn and -1."""
-    N, T1, V = target_probs.shape
-    T, dev = T1 - 1, target_probs.device
-    code = _dtype_code(target_probs)
-    _want("target_probs", target_probs, (N, T1, V), target_probs.dtype, dev)
-    if draft_probs is not None:
-        _want("draft_probs", draft_probs, (N, T, V), target_probs.dtype, dev)
-    _want("tokens", tokens, (N, T), torch.int32, dev)
-    if parents is not None:
-        _want("parents", parents, (N, T), torch.int32, dev)
-    _want("uniforms", uniforms, (N, T1), torch.float32, dev)
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
-    accept_node = new(N) if accept_node is None else accept_node
-    accept_len = new(N) if accept_len is None else accept_len
-    out_tokens = new(N, T1) if out_tokens is None else out_tokens
-    _want("accept_node", accept_node, (N,), torch.int32, dev)
-    _want("accept_len", accept_len, (N,), torch.int32, dev)
-    _want("out_tokens", out_tokens, (N, T1), torch.int32, dev)
-    _call("kda_verify_tree", dev, stream, target_probs.data_ptr(), _at(draft_probs),
-          tokens.data_ptr(), _at(parents), uniforms.data_ptr(), accept_node.data_ptr(),
-          accept_len.data_ptr(), out_tokens.data_ptr(), N, T, V, code)
+    st, accept_node, accept_len, out_tokens = (_native_module or _native()).verify_tree(
+        target_probs, draft_probs, tokens, parents, uniforms, accept_node, accept_len, out_tokens, _raw(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_verify_tree")
     return accept_node, accept_len, out_tokens
-
-
-_CACHE_CODES = {torch.float8_e4m3fn: KDA_CACHE_E4M3, torch.int8: KDA_CACHE_INT8}
-
-
-def _want_cache(states, slots, cache, scales):
-    n, H, Dk, Dv = states.shape
-    dev = states.device
-    code = _CACHE_CODES.get(cache.dtype)
-    if code is None:
-        raise TypeError(f"cache must be float8_e4m3fn or int8, got {cache.dtype}")
-    num_slots = cache.shape[0]
-    _want("states", states, (n, H, Dk, Dv), torch.float32, dev)
-    _want("slots", slots, (n,), torch.int32, dev)
-    _want("cache", cache, (num_slots, H, Dk, Dv), cache.dtype, dev)
-    _want("scales", scales, (num_slots, H, Dk), torch.float32, dev)
-    return num_slots, code, _shape(n, n, H, Dk, Dv, 0, KDA_DTYPE_F32)
 
 
 def kda_state_store(states, slots, cache, scales, *, stream=None):
@@ -499,21 +425,18 @@ def kda_state_store(states, slots, cache, scales, *, stream=None):
     (see kda_state_store in include/kda.h): cache [num_slots, H, Dk, Dv]
     (float8_e4m3fn or int8), scales [num_slots, H, Dk] FP32.  Returns (cache,
     scales)."""
-    num_slots, code, shape = _want_cache(states, slots, cache, scales)
-    _call("kda_state_store", states.device, stream, states.data_ptr(), slots.data_ptr(),
-          cache.data_ptr(), scales.data_ptr(), num_slots, code, ctypes.byref(shape))
+    st = (_native_module or _native()).state_store(states, slots, cache, scales, _raw(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_state_store")
     return cache, scales
 
 
 def kda_state_load(cache, scales, slots, *, states=None, stream=None):
     """Read the states of the slots slots[n] (outside the cache: the zero state)
     back from the state cache.  Returns states [n, H, Dk, Dv] FP32."""
-    if states is None:
-        states = torch.empty(slots.numel(), *cache.shape[1:], dtype=torch.float32,
-                             device=cache.device)
-    num_slots, code, shape = _want_cache(states, slots, cache, scales)
-    _call("kda_state_load", states.device, stream, cache.data_ptr(), scales.data_ptr(),
-          slots.data_ptr(), states.data_ptr(), num_slots, code, ctypes.byref(shape))
+    st, states = (_native_module or _native()).state_load(cache, scales, slots, states, _raw(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_state_load")
     return states
 
 
