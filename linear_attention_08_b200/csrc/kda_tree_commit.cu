@@ -17,7 +17,7 @@
 // barrier), takes them into registers when the unit begins, and starts the next
 // unit's copies into the same slots.  accept_node and parents are read two units
 // ahead, the path's first rows one unit ahead.  (Without this a CTA waited in turn
-// for accept_node, the state and the rows: 512 x 32 units in 416 us; 366 with it, 91 %
+// for accept_node, the state and the rows: 512 x 32 units in 416 us; 351 with it, 95 %
 // of the copy rate.)
 #include "kda_common.cuh"
 
@@ -33,9 +33,11 @@ template <int DK, int DV, typename TIn> struct CommitCfg {
   // 16-byte pieces of one token's g, k, v
   static constexpr int CG = DK / 4, CK = DK * (int)sizeof(TIn) / 16, CV = COLS * (int)sizeof(TIn) / 16;
   static constexpr int CT = CG + CK + CV;
-  static constexpr int SMEM = DK * COLS * 4 + kGroup * (DK * 8 + COLS * 4 + CT * 16 + 8);
+  // CTAs per SM by shared memory and by registers (the elements and about 56 more)
+  static constexpr int SMEM = DK * COLS * 4 + kGroup * (DK * 16 + COLS * 4 + CT * 16 + 8);
   static constexpr int FIT = 227 * 1024 / (SMEM + 1024);
-  static constexpr int PER_SM = FIT < 8 ? FIT : 8;
+  static constexpr int REGS = 65536 / (THREADS * (4 * ROWS + 56));
+  static constexpr int PER_SM = FIT < REGS ? FIT : REGS;
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
@@ -43,6 +45,30 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Two FP32 numbers per register pair: Blackwell's packed products take one instruction
+// for both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
 }
 
 // Place of the j-th token of a path, from the state on (a token's place is above its
@@ -61,10 +87,10 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
   using C = CommitCfg<DK, DV, TIn>;
   constexpr int COLS = C::COLS, PARTS = C::PARTS, THREADS = C::THREADS, ROWS = C::ROWS;
   constexpr int V4 = DV / 4;
-  __shared__ float4 s_state[ROWS][THREADS];   // the next unit's elements
+  __shared__ ulonglong2 s_state[ROWS][THREADS];   // the next unit's elements
   __shared__ uint4 s_raw[kGroup][C::CT];      // its path's first rows: g, k, v
   __shared__ float s_rb[kGroup];              // and beta
-  __shared__ float2 s_ak[kGroup][DK];         // (alpha, k)
+  __shared__ float4 s_ak[kGroup][DK];         // (alpha, alpha, k, k): pairs as they are used
   __shared__ float s_v[kGroup][COLS];
   __shared__ float s_b[kGroup];
 
@@ -105,11 +131,12 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
     const int64_t unit = item / PARTS;
     return unit / H * T * H + unit % H;
   };
-  const auto start_copies = [&](int64_t item, unsigned long long path) {
-    if (path == 0 && in_place) return;         // a state that is not touched
+  const auto start_state = [&](int64_t item) {
     const float4 *src = reinterpret_cast<const float4 *>(state) + elements(item);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) copy16(smem_u32(&s_state[i][tid]), src + i * 8 * V4);
+  };
+  const auto start_rows = [&](int64_t item, unsigned long long path) {
     const int m = min(kGroup, __popcll(path));
     const int64_t row0 = first_row(item);
     for (int e = tid; e < m * C::CT; e += THREADS) {
@@ -127,15 +154,17 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
 
   int64_t item = blockIdx.x;
   read_ahead(item);
+  if (!in_place) start_state(item);            // nothing of the path decides whether it is read
   unsigned long long path = find_path();
-  start_copies(item, path);
+  start_rows(item, path);
+  if (in_place && path != 0) start_state(item);
   read_ahead(item + G);
   for (; item < items; item += G) {
     const int64_t next = item + G;
     const unsigned long long next_path = next < items ? find_path() : 0ull;
     read_ahead(next + G);
     const bool active = path != 0 || !in_place;
-    float4 s[ROWS];
+    ulonglong2 s[ROWS];
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();                           // the others' copies of rows; the last unit's are used up
     if (active) {
@@ -145,24 +174,32 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
     int m = min(kGroup, __popcll(path));
     for (int e = tid; e < m * DK; e += THREADS) {
       const int j = e / DK, c = e % DK;
-      s_ak[j][c] = make_float2(expf(reinterpret_cast<const float *>(&s_raw[j][0])[c]),
-                               to_f32(reinterpret_cast<const TIn *>(&s_raw[j][C::CG])[c]));
+      const float al = expf(reinterpret_cast<const float *>(&s_raw[j][0])[c]);
+      const float kc = to_f32(reinterpret_cast<const TIn *>(&s_raw[j][C::CG])[c]);
+      s_ak[j][c] = make_float4(al, al, kc, kc);
     }
     for (int e = tid; e < m * COLS; e += THREADS)
       s_v[e / COLS][e % COLS] = to_f32(reinterpret_cast<const TIn *>(&s_raw[e / COLS][C::CG + C::CK])[e % COLS]);
     if (tid < m) s_b[tid] = s_rb[tid];
     __syncthreads();
-    if (next < items) start_copies(next, next_path);
+    if (next < items) {
+      if (!in_place || next_path != 0) start_state(next);
+      start_rows(next, next_path);
+    }
     if (active) {
       while (m > 0) {
         for (int j = 0; j < m; ++j) {
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          f32x2 ya = 0, yb = 0;
 #pragma unroll
           for (int i = 0; i < ROWS; ++i) {
-            const float2 ak = s_ak[j][ks + 8 * i];
-            s[i].x *= ak.x; s[i].y *= ak.x; s[i].z *= ak.x; s[i].w *= ak.x;
-            y.x += ak.y * s[i].x; y.y += ak.y * s[i].y; y.z += ak.y * s[i].z; y.w += ak.y * s[i].w;
+            const ulonglong2 ak = *reinterpret_cast<const ulonglong2 *>(&s_ak[j][ks + 8 * i]);
+            s[i].x = mul2(s[i].x, ak.x);
+            s[i].y = mul2(s[i].y, ak.x);
+            ya = fma2(ak.y, s[i].x, ya);
+            yb = fma2(ak.y, s[i].y, yb);
           }
+          const float2 y01 = unpack2(ya), y23 = unpack2(yb);
+          const float4 y = make_float4(y01.x, y01.y, y23.x, y23.y);
           // Sum over the 8 row residues: each step halves the columns a lane
           // keeps, so a lane ends with one column (7 shuffles, not 12).
           const bool b4 = lane & 16, b3 = lane & 8;
@@ -177,11 +214,13 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
           const float ua = b3 ? u8 : u, ub = b3 ? u : u8;
           const float ua16 = __shfl_xor_sync(0xffffffffu, ua, 16);
           const float ub16 = __shfl_xor_sync(0xffffffffu, ub, 16);
-          const float4 u4 = b4 ? make_float4(ua16, ub16, ua, ub) : make_float4(ua, ub, ua16, ub16);
+          const f32x2 u01 = b4 ? pack2(ua16, ub16) : pack2(ua, ub);
+          const f32x2 u23 = b4 ? pack2(ua, ub) : pack2(ua16, ub16);
 #pragma unroll
           for (int i = 0; i < ROWS; ++i) {
-            const float kc = s_ak[j][ks + 8 * i].y;
-            s[i].x += kc * u4.x; s[i].y += kc * u4.y; s[i].z += kc * u4.z; s[i].w += kc * u4.w;
+            const f32x2 kc = reinterpret_cast<const ulonglong2 *>(&s_ak[j][ks + 8 * i])->y;
+            s[i].x = fma2(kc, u01, s[i].x);
+            s[i].y = fma2(kc, u23, s[i].y);
           }
         }
         // the path's further tokens, read when they are needed
@@ -193,15 +232,20 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
         for (int e = tid; e < m * (DK + COLS); e += THREADS) {
           const int j = e / (DK + COLS), c = e % (DK + COLS);
           const int64_t row = row0 + (int64_t)nth(path, j) * H;
-          if (c < DK) s_ak[j][c] = make_float2(expf(g[row * DK + c]), to_f32(k[row * DK + c]));
-          else s_v[j][c - DK] = to_f32(v[row * DV + item % PARTS * COLS + (c - DK)]);
+          if (c < DK) {
+            const float al = expf(g[row * DK + c]), kc = to_f32(k[row * DK + c]);
+            s_ak[j][c] = make_float4(al, al, kc, kc);
+          } else s_v[j][c - DK] = to_f32(v[row * DV + item % PARTS * COLS + (c - DK)]);
           if (c == 0) s_b[j] = beta[row];
         }
         __syncthreads();
       }
       float4 *dst = reinterpret_cast<float4 *>(state_out) + elements(item);
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) __stcs(dst + i * 8 * V4, s[i]);
+      for (int i = 0; i < ROWS; ++i) {
+        const float2 a = unpack2(s[i].x), b = unpack2(s[i].y);
+        __stcs(dst + i * 8 * V4, make_float4(a.x, a.y, b.x, b.y));
+      }
     }
     path = next_path;
   }
