@@ -27,7 +27,7 @@
 // started (launch control): units of ragged trees differ in cost by a factor of two.
 // TP = 16: two CTAs of 128 + 32 threads per SM, so that one
 // computes while the other waits for a product.  TP = 32, 64: the buffers allow one CTA,
-// of 256 + 32 threads; X holds 32 tokens at a time.
+// of 256 + 32 threads; X holds 32 tokens, and the second 32 take the place of g.
 #include "kda_common.cuh"
 #include "kda_tc_util.cuh"
 #include "kda_tma.cuh"
@@ -55,8 +55,9 @@ template <int TP> struct TreeTc {
   static constexpr uint32_t X = SF + kD * kD * 4;        // [Kt; Qt] of a part: K-major tile
   static constexpr uint32_t AN = X;                      // before: A of the paths, K-major tile
   static constexpr uint32_t KH = X + XR * kD * 4;        // Kh: K-major tile of TP rows
-  static constexpr uint32_t KP = KH;                     // after: [KK; P], K-major tile
+  static constexpr uint32_t KP = NH == 1 ? KH : X;       // after: [KK; P], K-major tile
   static constexpr uint32_t RG = KH + TP * kD * 4;       // rows of g, q, k, v
+  static constexpr uint32_t X1 = RG;                     // after: X of part 1
   static constexpr uint32_t RQ = RG + TP * 512;
   static constexpr uint32_t RK = RQ + TP * 256;
   static constexpr uint32_t RV = RK + TP * 256;
@@ -70,12 +71,13 @@ template <int TP> struct TreeTc {
   static constexpr uint32_t QUIT = WIDE + 8;
   static constexpr uint32_t SLOT = QUIT + 4;
   static constexpr uint32_t BAR = SLOT + 4;
-  static constexpr uint32_t TOTAL = BAR + 12 * 8;
+  static constexpr uint32_t TOTAL = BAR + 14 * 8;
   static_assert(X % 1024 == 0 && KH % 1024 == 0 && NEXT % 16 == 0 && BAR % 8 == 0, "alignment");
-  static_assert(ROWS * 128 * ((TP + 31) / 32) <= TP * kD * 4, "[KK; P] in Kh's place");
+  static_assert(ROWS * 128 * ((TP + 31) / 32) <= (NH == 1 ? TP : XR) * kD * 4, "[KK; P]");
+  static_assert(NH == 1 || (RG % 1024 == 0 && XR * kD * 4 <= TP * 512), "X in g's place");
   static_assert(TP * 128 * ((TP + 31) / 32) <= XR * kD * 4, "A in X's place");
   // the A operand of D2 reads 128 rows, those past X into lanes that nobody reads
-  static_assert(X + (kD / 32 - 1) * XR * 128 + 128 * 128 <= TOTAL, "rows past the operand");
+  static_assert((NH == 1 ? X : X1) + (kD / 32 - 1) * XR * 128 + 128 * 128 <= TOTAL, "rows past the operand");
   // tensor memory, columns
   static constexpr uint32_t S = 0;                       // S0^T
   static constexpr uint32_t D1 = 128;                    // part by part: Kt S0, Qt S0
@@ -88,7 +90,8 @@ template <int TP> struct TreeTc {
 };
 
 enum TreeBar {
-  kFullQkg, kFullV, kFullS, kEmptyQkg, kEmptyV, kEmptyS, kMmaG, kMmaA, kMmaB, kMmaU, kMmaO, kNext, kBars
+  kFullQkg, kFullV, kFullS, kEmptyQkg, kEmptyV, kEmptyS, kMmaG, kMmaA, kMmaB,
+  kMmaA1, kMmaB1, kMmaU, kMmaO, kNext, kBars
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
@@ -381,7 +384,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     const __nv_bfloat16 *rq = reinterpret_cast<const __nv_bfloat16 *>(sp + C::RQ) + col;
     const __nv_bfloat16 *rk = reinterpret_cast<const __nv_bfloat16 *>(sp + C::RK) + col;
     const __nv_bfloat16 *rv = reinterpret_cast<const __nv_bfloat16 *>(sp + C::RV) + col;
-    const uint64_t x_desc = tc::desc_kmajor(sb + C::X, C::XR, 0);
+    const uint64_t x_desc[2] = {tc::desc_kmajor(sb + C::X, C::XR, 0), tc::desc_kmajor(sb + C::X1, C::XR, 0)};
     const uint64_t an_desc = tc::desc_kmajor(sb + C::AN, TP, 0);
     const uint64_t kh_desc = tc::desc_kmajor(sb + C::KH, TP, 0);
     const uint64_t kp_desc = tc::desc_kmajor(sb + C::KP, C::ROWS, 0);
@@ -497,17 +500,13 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
 #pragma unroll
       for (int hf = 0; hf < C::NH; ++hf) {
         if (hf > 0 && hf >= nh) break;
-        if (hf > 0) {                      // the products before have read X
-          done(kMmaA);
-          done(kMmaB);
-        }
         const int j0 = kBlk * hw, t0 = C::TH * hf + j0;
         if (t0 < kBlk * nb) {
           float Gt[kBlk];
           tc::tmem_ld16(tl + C::D3 + (uint32_t)t0, Gt);
           tc::tmem_wait_ld();
           const uint32_t within = (uint32_t)(((col & 31) >> 2) << 4);
-          uint8_t *xt = sp + C::X + (col >> 5) * C::XR * 128 + j0 * 128 + (col & 3) * 4;
+          uint8_t *xt = sp + (hf == 0 ? C::X : C::X1) + (col >> 5) * C::XR * 128 + j0 * 128 + (col & 3) * 4;
           uint8_t *kt = sp + C::KH + (col >> 5) * TP * 128 + t0 * 128 + (col & 3) * 4;
 #pragma unroll
           for (int j = 0; j < kBlk; ++j) {
@@ -523,7 +522,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           }
         }
         if (wide) s_wide[ph] = 1;
-        if (hf + 1 >= nh) release(kEmptyQkg);
+        if (C::NH == 1 || nh <= 1) release(kEmptyQkg);
         else tc::fence_smem_to_async();
         tc::fence_before_sync();
         if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
@@ -532,20 +531,20 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           tc::fence_after_sync();
 #pragma unroll
           for (int s = 0; s < kD / 8; ++s)
-            mma_tf32_ss(tmem + C::D2 + C::TH * hf, step_desc(x_desc, C::XR, s),
+            mma_tf32_ss(tmem + C::D2 + C::TH * hf, step_desc(x_desc[hf], C::XR, s),
                         step_desc(kh_desc, TP, s), idesc_tf32(128, C::TH * (hf + 1)), s > 0);
-          tc::mma_commit(bar_at(kMmaA));
+          tc::mma_commit(bar_at(hf == 0 ? kMmaA : kMmaA1));
         } else if (warp == 2 && elect_one()) {
           tc::fence_after_sync();
 #pragma unroll
           for (int s = 0; s < kD / 8; ++s)
             mma_tf32_ts(tmem + C::D1 + C::XR * hf, tmem + C::S + 8 * s,
-                        step_desc(x_desc, C::XR, s), idesc_tf32(128, C::XR), s > 0);
-          tc::mma_commit(bar_at(kMmaB));
+                        step_desc(x_desc[hf], C::XR, s), idesc_tf32(128, C::XR), s > 0);
+          tc::mma_commit(bar_at(hf == 0 ? kMmaB : kMmaB1));
         }
         __syncwarp();
-        pend |= 1u << kMmaA | 1u << kMmaB;
-        if (hf == 0 && i > 0) put_out();   // the last unit's outputs, while the products run
+        pend |= hf == 0 ? 1u << kMmaA | 1u << kMmaB : 1u << kMmaA1 | 1u << kMmaB1;
+        if (hf + 1 >= nh && i > 0) put_out();   // the last unit's outputs, while the products run
       }
       if (aborted) break;
 
@@ -553,11 +552,13 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       //      below it for P ----
       const bool pairwise = s_wide[ph] != 0;
       done(kMmaA);
+      if (C::NH > 1) done(kMmaB);          // the tile takes X's place
       if (tid == 0) s_wide[ph ^ 1] = 0;
       if (!pairwise) {
 #pragma unroll
         for (int hf = 0; hf < C::NH; ++hf) {
           constexpr int HALF = C::TH / C::WG;        // 16 columns; twice that in part 1
+          if (hf > 0 && hf < nh) done(kMmaA1);
           if (hf < nh && col < C::XR) {              // whole warps
             const int t = C::TH * hf + (col & (C::TH - 1));
             unsigned long long on = s_anc[t];
@@ -582,6 +583,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           }
         }
       } else {
+        if (C::NH > 1 && nh > 1) done(kMmaA1);
         // One warp per place: the path upwards, with the decay between its ends summed
         // from the near one, so that no large sums are subtracted.
         for (int t = warp; t < kBlk * nb; t += C::WORKERS / 32) {
@@ -624,7 +626,11 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
       }
       tc::fence_smem_to_async();
       bad |= !wait_timed(bars + kFullV, ph, wait_ns);
-      done(kMmaB);
+      if (C::NH == 1) done(kMmaB);
+      if (C::NH > 1 && nh > 1) {
+        done(kMmaB1);
+        release(kEmptyQkg);                // X of part 1 lay in g's place
+      }
       tc::fence_before_sync();
       if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
       tc::fence_after_sync();
@@ -643,16 +649,20 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
 #pragma unroll
           for (int j = 0; j < kBlk; ++j) {
             if (j == kBlk / 2 && kBlk * b + j >= last) break;
-            float a = __bfloat162float(rv[(kBlk * b + j) * kD]) - ks[j];
+            // four sums, and u of the token before last: short chains
+            float a = __bfloat162float(rv[(kBlk * b + j) * kD]) - ks[j], a1 = 0.f, a2 = 0.f, a3 = 0.f, end = 0.f;
 #pragma unroll
             for (int s4 = 0; s4 < j; s4 += 4) {
               const uint32_t at = (uint32_t)(j * 128) + ((uint32_t)(((s4 >> 2) ^ (j & 7)) << 4) ^ flip);
               const float4 kk = *reinterpret_cast<const float4 *>(kp + at);
-              a -= kk.x * x[s4];
-              if (s4 + 1 < j) a -= kk.y * x[s4 + 1];
-              if (s4 + 2 < j) a -= kk.z * x[s4 + 2];
-              if (s4 + 3 < j) a -= kk.w * x[s4 + 3];
+              if (s4 < j - 1) a -= kk.x * x[s4];
+              if (s4 + 1 < j - 1) a1 -= kk.y * x[s4 + 1];
+              if (s4 + 2 < j - 1) a2 -= kk.z * x[s4 + 2];
+              if (s4 + 3 < j - 1) a3 -= kk.w * x[s4 + 3];
+              if (s4 + 4 >= j) end = (j - 1) % 4 == 0 ? kk.x : (j - 1) % 4 == 1 ? kk.y : (j - 1) % 4 == 2 ? kk.z : kk.w;
             }
+            a = (a + a1) + (a2 + a3);
+            if (j > 0) a -= end * x[j > 0 ? j - 1 : 0];
             x[j] = s_beta[kBlk * b + j] * a;
           }
 #pragma unroll
@@ -661,16 +671,17 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           tc::tmem_wait_st();
           tc::fence_before_sync();
           asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
-          if (tid == 0) {
+          if (warp == 0 && elect_one()) {
             // tokens of this part and the later ones
             tc::fence_after_sync();
-            const uint32_t id = idesc_tf32(128, C::XR * (C::NH > 1 && nh > part + 1 ? 2 : 1));
             const uint64_t d = step_desc(kp_desc, C::ROWS, kBlk / 8 * b) + (uint64_t)(C::XR * part * 128 >> 4);
+            const uint32_t id = C::NH > 1 && nh > part + 1 ? idesc_tf32(128, 2 * C::XR) : idesc_tf32(128, C::XR);
 #pragma unroll
             for (int s = 0; s < kBlk / 8; ++s)
               mma_tf32_ts(tmem + C::D1 + C::XR * part, tmem + C::U + 8 * s, d + (uint64_t)(2 * s), id, 1);
             tc::mma_commit(bar_at(b + 1 < nb ? kMmaU : kMmaO));
           }
+          __syncwarp();
           if (b + 1 < nb) {
             pend |= 1u << kMmaU;
             done(kMmaU);
