@@ -34,6 +34,7 @@
 // inputs split each operand in two TF32 terms and add three products, and carry
 // Gam as an unevaluated sum of two FP32 numbers, for FP32 accuracy.
 #include "kda_common.cuh"
+#include "kda_launch.cuh"
 
 namespace kda {
 namespace {
@@ -178,6 +179,8 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   const int gid = lane >> 2, j = lane & 3;
   const int64_t row0 = (int64_t)n * T * H + h;      // token t is row row0 + t H
 
+  launch_dependents();
+  wait_for_inputs();
   int up[T8 > 32 ? 2 : 1];             // predecessors of places lane (and lane + 32)
   if (warp == 0) {
 #pragma unroll
@@ -607,9 +610,8 @@ cudaError_t launch_nt(const void *q, const void *k, const void *v, const float *
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::BYTES);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)units, Cfg::THREADS, Cfg::BYTES, stream>>>(
-      (const TIn *)q, (const TIn *)k, (const TIn *)v, g, beta, state, parents, (TIn *)out, T, H);
-  return cudaGetLastError();
+  return launch_dependent(kern, (unsigned)units, Cfg::THREADS, Cfg::BYTES, 1, stream, (const TIn *)q,
+                          (const TIn *)k, (const TIn *)v, g, beta, state, parents, (TIn *)out, T, H);
 }
 
 template <int DK, int DV, typename TIn>

@@ -29,6 +29,7 @@
 // computes while the other waits for a product.  TP = 32, 64: the buffers allow one CTA,
 // of 256 + 32 threads; X holds 32 tokens, and the second 32 take the place of g.
 #include "kda_common.cuh"
+#include "kda_launch.cuh"
 #include "kda_tc_util.cuh"
 #include "kda_tma.cuh"
 
@@ -220,6 +221,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be uniform
   const auto bar_at = [&](int b) { return sb + C::BAR + 8 * b; };
 
+  launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i)   // rows: a lane's copies each, and the masks
       mbar_init(bars + i, i == kEmptyQkg || i == kEmptyV || i == kEmptyS ? C::WORKERS / 32
@@ -234,6 +236,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sp + C::SLOT), 0);
+  wait_for_inputs();
 
   if (warp == C::WORKERS / 32) {
     // ------------------------------------------------------------ producer
@@ -733,10 +736,9 @@ cudaError_t launch_tp(const void *q, const void *k, const void *v, const float *
   e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                            (int)cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)units, C::THREADS, smem, stream>>>(
-      (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k, (const __nv_bfloat16 *)v, g, beta, state,
-      parents, (__nv_bfloat16 *)out, T, H, dev_status, 2000000000ull);
-  return cudaGetLastError();
+  return launch_dependent(kern, (unsigned)units, C::THREADS, smem, 1, stream, (const __nv_bfloat16 *)q,
+                          (const __nv_bfloat16 *)k, (const __nv_bfloat16 *)v, g, beta, state, parents,
+                          (__nv_bfloat16 *)out, T, H, dev_status, 2000000000ull);
 }
 
 }  // namespace

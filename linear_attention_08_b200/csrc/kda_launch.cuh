@@ -1,0 +1,42 @@
+// Launches that may begin before the kernel ahead of them in the stream has ended
+// (programmatic dependent launch), for kernels that take a few microseconds.
+//
+// Such a kernel's blocks are started as soon as every block of the kernel ahead has
+// called launch_dependents() or ended; they set up their shared and tensor memory, and
+// wait_for_inputs() returns once the kernel ahead has completed and its writes are
+// visible.  No global memory is touched before that.  A kernel ahead that does not call
+// launch_dependents() has the usual order.  One user's calls in a row: tree decode 8.2 ->
+// MEASURE us.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace kda {
+
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem,
+                             unsigned cluster, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kda

@@ -24,6 +24,7 @@
 #include <math_constants.h>
 
 #include "kda_common.cuh"
+#include "kda_launch.cuh"
 
 namespace kda {
 namespace {
@@ -121,6 +122,8 @@ state_store_kernel(const float *__restrict__ states, const int32_t *__restrict__
   const int64_t unit = blockIdx.x;
   const int n = (int)(unit / H), h = (int)(unit % H);
   const int tid = threadIdx.x, cg = tid % V4, rg = tid / V4;
+  launch_dependents();
+  wait_for_inputs();
   const int32_t slot = slots[n];
   if (slot < 0 || (int64_t)slot >= num_slots) return;
   const float4 *src = reinterpret_cast<const float4 *>(states) + unit * (DK * V4);
@@ -163,6 +166,8 @@ state_load_kernel(const uint32_t *__restrict__ cache, const float *__restrict__ 
   const int64_t unit = blockIdx.x;
   const int n = (int)(unit / H), h = (int)(unit % H);
   const int tid = threadIdx.x, cg = tid % V4, rg = tid / V4;
+  launch_dependents();
+  wait_for_inputs();
   const int32_t slot = slots[n];
   float4 *dst = reinterpret_cast<float4 *>(states) + unit * (DK * V4);
   if (slot < 0 || (int64_t)slot >= num_slots) {   // no cached prefix: the zero state
@@ -190,15 +195,11 @@ cudaError_t launch_d(bool store, bool e4m3, float *states, const int32_t *slots,
                      float *scales, int N, int H, int64_t num_slots, cudaStream_t stream) {
   const unsigned grid = (unsigned)((int64_t)N * H);
   uint32_t *c = static_cast<uint32_t *>(cache);
-  if (store && e4m3)
-    state_store_kernel<DK, DV, true><<<grid, kCacheThreads, 0, stream>>>(states, slots, c, scales, N, H, num_slots);
-  else if (store)
-    state_store_kernel<DK, DV, false><<<grid, kCacheThreads, 0, stream>>>(states, slots, c, scales, N, H, num_slots);
-  else if (e4m3)
-    state_load_kernel<DK, DV, true><<<grid, kCacheThreads, 0, stream>>>(c, scales, slots, states, H, num_slots);
-  else
-    state_load_kernel<DK, DV, false><<<grid, kCacheThreads, 0, stream>>>(c, scales, slots, states, H, num_slots);
-  return cudaGetLastError();
+  if (store)
+    return launch_dependent(e4m3 ? state_store_kernel<DK, DV, true> : state_store_kernel<DK, DV, false>, grid,
+                            kCacheThreads, 0, 1, stream, states, slots, c, scales, N, H, num_slots);
+  return launch_dependent(e4m3 ? state_load_kernel<DK, DV, true> : state_load_kernel<DK, DV, false>, grid,
+                          kCacheThreads, 0, 1, stream, c, scales, slots, states, H, num_slots);
 }
 
 }  // namespace

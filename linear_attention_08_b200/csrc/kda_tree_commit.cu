@@ -20,6 +20,7 @@
 // for accept_node, the state and the rows: 512 x 32 units in 416 us; 351 with it, 95 %
 // of the copy rate.)
 #include "kda_common.cuh"
+#include "kda_launch.cuh"
 
 namespace kda {
 namespace {
@@ -152,6 +153,8 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
     if (tid < m) copy4(smem_u32(&s_rb[tid]), beta + row0 + (int64_t)nth(path, tid) * H);
   };
 
+  launch_dependents();
+  wait_for_inputs();
   int64_t item = blockIdx.x;
   read_ahead(item);
   if (!in_place) start_state(item);            // nothing of the path decides whether it is read
@@ -268,10 +271,10 @@ cudaError_t launch_t(int dk, int dv, const void *k, const void *v, const float *
                                                cudaFuncAttributePreferredSharedMemoryCarveout,    \
                                                (int)cudaSharedmemCarveoutMaxShared);              \
     if (e != cudaSuccess) return e;                                                               \
-    tree_commit_kernel<DK_, DV_, TIn><<<(unsigned)(items < slots ? items : slots), C::THREADS, 0, \
-                                        stream>>>((const TIn *)k, (const TIn *)v, g, beta, state, \
-                                                  state_out, parents, accept_node, T, H, items);  \
-    return cudaGetLastError();                                                                    \
+    return launch_dependent(tree_commit_kernel<DK_, DV_, TIn>,                                    \
+                            (unsigned)(items < slots ? items : slots), C::THREADS, 0, 1, stream,  \
+                            (const TIn *)k, (const TIn *)v, g, beta, state, state_out, parents,   \
+                            accept_node, T, H, items);                                            \
   }
   KDA_TC(32, 32) KDA_TC(32, 64) KDA_TC(32, 128)
   KDA_TC(64, 32) KDA_TC(64, 64) KDA_TC(64, 128)

@@ -36,6 +36,7 @@
 #include <cooperative_groups.h>
 
 #include "kda_common.cuh"
+#include "kda_launch.cuh"
 
 namespace kda {
 namespace {
@@ -230,6 +231,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   __shared__ double s_tot[2][kVMaxCluster];   // the CTAs' sums, one buffer per parity of the pass
   __shared__ int s_last[kVWarps];
 
+  launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   if (CS > 1) cluster.barrier_arrive();   // the others' shared memory exists once all have started
@@ -246,6 +248,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     return (int)(b < vocab ? b : vocab);
   };
 
+  wait_for_inputs();
   if (tid <= T) s_u[tid] = uniforms[n * (T + 1) + tid];
   if (tid < T) {
     const int x = tokens[n * T + tid];
@@ -417,27 +420,14 @@ cudaError_t launch_verify_tree(bool bf16, const void *target, const void *draft,
   int cs = kVMaxCluster;
   const int least = kVThreads * (bf16 ? kVec<__nv_bfloat16> : kVec<float>);
   while (cs > 1 && ((int64_t)N * cs > 2 * (int64_t)num_sms || vocab <= (cs / 2) * least)) cs >>= 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)N * cs));
-  cfg.blockDim = dim3(kVThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e;
+  const unsigned grid = (unsigned)((int64_t)N * cs);
   if (bf16)
-    e = cudaLaunchKernelEx(&cfg, verify_tree_kernel<__nv_bfloat16>, (const __nv_bfloat16 *)target,
-                           (const __nv_bfloat16 *)draft, tokens, parents, uniforms, accept_node,
-                           accept_len, out_tokens, T, vocab);
-  else
-    e = cudaLaunchKernelEx(&cfg, verify_tree_kernel<float>, (const float *)target,
-                           (const float *)draft, tokens, parents, uniforms, accept_node,
-                           accept_len, out_tokens, T, vocab);
-  return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(verify_tree_kernel<__nv_bfloat16>, grid, kVThreads, 0, (unsigned)cs, stream,
+                            (const __nv_bfloat16 *)target, (const __nv_bfloat16 *)draft, tokens, parents,
+                            uniforms, accept_node, accept_len, out_tokens, T, vocab);
+  return launch_dependent(verify_tree_kernel<float>, grid, kVThreads, 0, (unsigned)cs, stream,
+                          (const float *)target, (const float *)draft, tokens, parents, uniforms,
+                          accept_node, accept_len, out_tokens, T, vocab);
 }
 
 }  // namespace kda
