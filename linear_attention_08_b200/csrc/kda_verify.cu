@@ -216,6 +216,26 @@ __device__ __forceinline__ double rest_one(const Rest &rest, float p, float d, i
   return r[0][0] * kUnscale;
 }
 
+// The part that the border lies in, of N whose sums the lanes hold: the first whose
+// cumulative sum, from `base` on, passes it, else the last with anything in it (a random
+// number of 1), -1 when there is none.  `before`: the sum ahead of it.  Whole warps.
+template <int N>
+__device__ __forceinline__ int find_part(double mine, double base, double border, double &before) {
+  const int lane = threadIdx.x & 31;
+  double incl = mine;
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
+  const uint32_t past = __ballot_sync(0xffffffffu, mine > 0.0 && base + incl > border);
+  const int part = past ? __ffs(past) - 1 : 31 - __clz(some);
+  const double ahead = __shfl_sync(0xffffffffu, incl, part > 0 ? part - 1 : 0);
+  before = base + (part > 0 ? ahead : 0.0);
+  return part;
+}
+
 template <typename P>
 __global__ void __launch_bounds__(kVThreads, 2)
 verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
@@ -335,26 +355,14 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
   // The CTA, then the warp slice, that the border lies in: the first whose
   // cumulative sum passes it, else (a random number of 1) the last with a part.
   const double border = (double)s_u[T] * total;
-  int owner = -1, wown = 0;
-  double before = 0.0, run = 0.0;
-  bool found = false;
-  for (int i = 0; i < CS; ++i) {
-    const double t = s_tot[buf][i];
-    if (!found && t > 0.0) { owner = i; before = run; found = run + t > border; }
-    run += t;
-  }
+  double before;
+  const int owner = find_part<kVMaxCluster>(lane < CS ? s_tot[buf][lane] : 0.0, 0.0, border, before);
   if (owner < 0) {   // no token has a probability
     if (rank == 0 && tid == 0) out_tokens[n * (T + 1) + count] = -1;
     return;
   }
   if (owner != rank) return;
-  run = before;
-  found = false;
-  for (int i = 0; i < kVWarps; ++i) {
-    const double t = s_warp[i];
-    if (!found && t > 0.0) { wown = i; before = run; found = run + t > border; }
-    run += t;
-  }
+  const int wown = max(0, find_part<kVWarps>(lane < kVWarps ? s_warp[lane] : 0.0, before, border, before));
   // The warp slice over the whole CTA: a contiguous piece per thread, its sum,
   // the threads' prefix sums, then the one piece that holds the border.
   const int lo = bound(rank * kVWarps + wown), hi = bound(rank * kVWarps + wown + 1);
@@ -375,18 +383,19 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     const double x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
-  int wlast = last;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wlast = max(wlast, __shfl_xor_sync(0xffffffffu, wlast, o));
+  const int wlast = __reduce_max_sync(0xffffffffu, last);
   if (lane == 31) s_scan[warp] = incl;
   if (lane == 0) s_last[warp] = wlast;
   __syncthreads();
-  double start = before;
-  int all_last = -1;
-  for (int i = 0; i < kVWarps; ++i) {
-    if (i < warp) start += s_scan[i];
-    all_last = max(all_last, s_last[i]);
+  double all = lane < kVWarps ? s_scan[lane] : 0.0;    // the warps' sums up to each
+#pragma unroll
+  for (int o = 1; o < kVWarps; o <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += x;
   }
+  const double ahead = __shfl_sync(0xffffffffu, all, warp > 0 ? warp - 1 : 0);
+  const double start = before + (warp > 0 ? ahead : 0.0);
+  const int all_last = __reduce_max_sync(0xffffffffu, lane < kVWarps ? s_last[lane] : -1);
   // first token whose cumulative sum passes the border, or the slice's last
   int hit = INT32_MAX;
   double c = start + (incl - mine);
@@ -395,8 +404,7 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     c += r;
     if (r > 0.0 && c > border) { hit = i; break; }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) hit = min(hit, __shfl_xor_sync(0xffffffffu, hit, o));
+  hit = __reduce_min_sync(0xffffffffu, hit);
   __syncthreads();
   if (lane == 0) s_last[warp] = hit;
   __syncthreads();
