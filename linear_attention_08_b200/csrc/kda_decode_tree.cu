@@ -91,44 +91,26 @@ __device__ __forceinline__ void mma(float (&c)[4], const Op<X3> &a0, const Op<X3
 // 8 i + 2 j + e, touch distinct banks.
 __device__ __forceinline__ int swizzle(int row) { return ((row & 6) ^ ((row & 1) << 2)); }
 
-// E consecutive elements as floats (2 or 4).
-template <int E> __device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float *x) {
-  uint32_t w[E / 2];
-  if (E == 4) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-    w[0] = u.x;
-    w[E / 2 - 1] = u.y;
-  } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+// Two consecutive elements, as loaded and as floats.
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+  uint32_t x = 0u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { x = __ldg(reinterpret_cast<const uint32_t *>(p)); }
+  __device__ __forceinline__ float2 get() const {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
   }
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+};
+template <> struct Pair<float> {
+  float2 x = {0.f, 0.f};
+  __device__ __forceinline__ void load(const float *p) { x = __ldg(reinterpret_cast<const float2 *>(p)); }
+  __device__ __forceinline__ float2 get() const { return x; }
+};
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(&h);
 }
-template <int E> __device__ __forceinline__ void load_row(const float *p, float *x) {
-  if (E == 4) {
-    const float4 u = __ldg(reinterpret_cast<const float4 *>(p));
-    x[0] = u.x; x[1] = u.y; x[E - 2] = u.z; x[E - 1] = u.w;
-  } else {
-    const float2 u = __ldg(reinterpret_cast<const float2 *>(p));
-    x[0] = u.x; x[1] = u.y;
-  }
-}
-template <int E> __device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float *x) {
-  uint32_t w[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t *>(&b);
-  }
-  if (E == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[E / 2 - 1]);
-  else *reinterpret_cast<uint32_t *>(p) = w[0];
-}
-template <int E> __device__ __forceinline__ void store_row(float *p, const float *x) {
-  if (E == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[E - 2], x[E - 1]);
-  else *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+__device__ __forceinline__ void store_pair(float *p, float a, float b) {
+  *reinterpret_cast<float2 *>(p) = make_float2(a, b);
 }
 
 // Sets of places: 32 bits do for up to four tiles.
@@ -138,9 +120,10 @@ template <> struct MaskOf<8> { using T = unsigned long long; };
 // NT: tiles of 8 places (places past T are empty ones).
 template <int DK, int DV, int NT, typename TIn> struct TreeCfg {
   static constexpr bool X3 = sizeof(TIn) == 4;
-  static constexpr int MT = 1;  // 16-column tiles per warp (registers)
-  static constexpr int E = 2 * MT;                  // value columns, or key channels, per lane
-  static constexpr int WARPS = DV / (16 * MT);
+  static constexpr int WARPS = DV / 16;             // 16 value columns each, two per lane
+  // Rows are loaded into registers as soon as the paths are known, all at once, as long
+  // as there are registers for them.
+  static constexpr bool AHEAD = NT <= 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int T8 = 8 * NT;
   static constexpr int NB = NT < 2 ? 1 : NT / 2;    // diagonal blocks
@@ -165,7 +148,8 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   using Cfg = TreeCfg<DK, DV, NT, TIn>;
   using Mask = typename MaskOf<NT>::T;
   constexpr bool X3 = Cfg::X3;
-  constexpr int MT = Cfg::MT, E = Cfg::E, T8 = Cfg::T8, LDT = Cfg::LDT;
+  constexpr int T8 = Cfg::T8, LDT = Cfg::LDT, E = 2;
+  constexpr bool AHEAD = Cfg::AHEAD;
   constexpr int LDB = Cfg::LDB, BT = Cfg::BT, NB = Cfg::NB;
   extern __shared__ __align__(16) float sm[];
   float *s_kt = sm + Cfg::KT, *s_qt = sm + Cfg::QT, *s_kh = sm + Cfg::KH;
@@ -182,32 +166,30 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   launch_dependents();
   wait_for_inputs();
   int up[T8 > 32 ? 2 : 1];             // predecessors of places lane (and lane + 32)
+  float bt[T8 > 32 ? 2 : 1];
   if (warp == 0) {
 #pragma unroll
     for (int e = 0; e < (T8 > 32 ? 2 : 1); ++e) {
       const int t = lane + 32 * e;
       up[e] = -2;
-      if (t < T) up[e] = parents ? __ldg(parents + (int64_t)n * T + t) : t - 1;
+      bt[e] = 0.f;
+      if (t < T) {
+        up[e] = parents ? __ldg(parents + (int64_t)n * T + t) : t - 1;
+        bt[e] = __ldg(beta + row0 + (int64_t)t * H);
+      }
     }
   }
 
-  // ---- the state's columns of this warp: rows 16 a + 4 j + m, columns col .. col + E - 1 ----
-  const int col = 16 * MT * warp + E * gid;
+  // ---- the state's columns of this warp: rows 16 a + 4 j + m, columns col, col + 1 ----
+  const int col = 16 * warp + E * gid;
   float s0[DK / 4][E];
   {
     const float *src = state + unit * (DK * DV) + (int64_t)(4 * j) * DV + col;
 #pragma unroll
-    for (int m = 0; m < DK / 4; ++m) {
-      const float *at = src + ((m >> 2) * 16 + (m & 3)) * DV;
-      if (E == 4)
-        asm volatile("ld.global.cs.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(s0[m][0]), "=f"(s0[m][1]), "=f"(s0[m][E - 2]), "=f"(s0[m][E - 1])
-                     : "l"(at));
-      else
-        asm volatile("ld.global.cs.v2.f32 {%0,%1}, [%2];"
-                     : "=f"(s0[m][0]), "=f"(s0[m][1])
-                     : "l"(at));
-    }
+    for (int m = 0; m < DK / 4; ++m)
+      asm volatile("ld.global.cs.v2.f32 {%0,%1}, [%2];"
+                   : "=f"(s0[m][0]), "=f"(s0[m][1])
+                   : "l"(src + ((m >> 2) * 16 + (m & 3)) * DV));
   }
 
   // ---- ancestors by pointer doubling (one warp): after the step of size d every
@@ -260,75 +242,99 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
     __syncwarp();
     // tiles up to the last token that is there; the rest is not computed
     int last = -1;
-    for (int t = lane; t < T8; t += 32) {
-      const bool live = s_anc[t] != 0;
-      s_beta[t] = live ? beta[row0 + (int64_t)t * H] : 0.f;
-      if (live) last = t;
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+    for (int e = 0; e < (T8 > 32 ? 2 : 1); ++e) {
+      const int t = lane + 32 * e;
+      if (t < T8) {
+        const bool live = s_anc[t] != 0;
+        s_beta[t] = live ? bt[e] : 0.f;
+        if (live) last = t;
+      }
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) s_tiles = (last + 8) >> 3;
   }
   __syncthreads();
   const int tiles = s_tiles;
 
-  // ---- Gam along the paths, Kt, Qt, Kh.  Gam^T = g^T A^T with A the 0/1 matrix of
-  //      ancestors, a product as well: a lane brings g, and gets Gam, of places
-  //      8 i + 2 j, + 1 in E channels.  g goes in as two TF32 terms (2^-23 of it is
-  //      lost); for X3 as multiples of 1/8, whose sums are exact, and two terms for
-  //      the rest, with sums of their own. ----
-  bool wide = false;   // factors out of range: L and P pair by pair
-  for (int cw = warp; cw < DK / (16 * MT); cw += Cfg::WARPS) {
-    const int c0 = 16 * MT * cw + E * gid;
-    float gam[NT][MT][4], low[X3 ? NT : 1][MT][4];
+  // The lane's places 8 i + 2 j + e.
+  const auto place = [&](int i, int e) { return 8 * i + 2 * j + e; };
+  const TIn *vp = v + row0 * DV + col;
+  Pair<TIn> rv[AHEAD ? 2 * NT : 1];
+  if (AHEAD) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int e = 0; e < 2; ++e)
+        if (i < tiles && s_anc[place(i, e)] != 0) rv[AHEAD ? 2 * i + e : 0].load(vp + (int64_t)place(i, e) * H * DV);
+  }
+
+  // ---- Gam along the paths, Kt, Qt, Kh.  Gam^T = g^T A^T with A the 0/1 matrix of
+  //      ancestors, a product as well: a lane brings g, and gets Gam, of its places
+  //      in two channels.  g goes in as two TF32 terms (2^-23 of it is
+  //      lost); for X3 as multiples of 1/8, whose sums are exact, and two terms for
+  //      the rest, with sums of their own. ----
+  bool wide = false;   // factors out of range: L and P pair by pair
+  for (int cw = warp; cw < DK / 16; cw += Cfg::WARPS) {
+    const int c0 = 16 * cw + E * gid;
+    const int64_t at0 = row0 * DK + c0, step = (int64_t)H * DK;
+    Pair<float> rg[AHEAD ? 2 * NT : 1];
+    Pair<TIn> rk[AHEAD ? 2 * NT : 1], rq[AHEAD ? 2 * NT : 1];
+    if (AHEAD) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          gam[i][m][e] = 0.f;
-          if (X3) low[X3 ? i : 0][m][e] = 0.f;
-        }
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (i < tiles && s_anc[place(i, e)] != 0) {
+            const int64_t at = at0 + place(i, e) * step;
+            rg[AHEAD ? 2 * i + e : 0].load(g + at);
+            rk[AHEAD ? 2 * i + e : 0].load(k + at);
+            rq[AHEAD ? 2 * i + e : 0].load(q + at);
+          }
+    }
+    float gam[NT][4], low[X3 ? NT : 1][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gam[i][e] = 0.f;
+        if (X3) low[X3 ? i : 0][e] = 0.f;
+      }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       if (i >= tiles) break;
       float x[2][E];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int t = 8 * i + 2 * j + e;
-#pragma unroll
-        for (int c = 0; c < E; ++c) x[e][c] = 0.f;
-        if (s_anc[t] != 0) load_row<E>(g + (row0 + (int64_t)t * H) * DK + c0, x[e]);
+        Pair<float> y;
+        if (AHEAD) y = rg[AHEAD ? 2 * i + e : 0];
+        else if (s_anc[place(i, e)] != 0) y.load(g + at0 + place(i, e) * step);
+        x[e][0] = y.get().x;
+        x[e][1] = y.get().y;
       }
-      uint32_t hi[MT][4], lo[MT][4], lo2[MT][4];
+      uint32_t hi[4], lo[4], lo2[4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y = x[e >> 1][2 * m + (e & 1)];   // a0, a1: place 2 j; a2, a3: place 2 j + 1
-          if (X3) {
-            y = fmaxf(y, -128.f);                 // exp(-128) is 0 in FP32 already
-            const float r = rintf(y * 8.f) * 0.125f;
-            hi[m][e] = __float_as_uint(r);
-            y -= r;
-            lo[m][e] = tf32_rn(y);
-            lo2[m][e] = tf32_rn(y - __uint_as_float(lo[m][e]));
-          } else {
-            hi[m][e] = tf32_rn(y);
-            lo[m][e] = tf32_rn(y - __uint_as_float(hi[m][e]));
-          }
+      for (int e = 0; e < 4; ++e) {
+        float y = x[e >> 1][e & 1];             // a0, a1: place 2 j; a2, a3: place 2 j + 1
+        if (X3) {
+          y = fmaxf(y, -128.f);                 // exp(-128) is 0 in FP32 already
+          const float r = rintf(y * 8.f) * 0.125f;
+          hi[e] = __float_as_uint(r);
+          y -= r;
+          lo[e] = tf32_rn(y);
+          lo2[e] = tf32_rn(y - __uint_as_float(lo[e]));
+        } else {
+          hi[e] = tf32_rn(y);
+          lo[e] = tf32_rn(y - __uint_as_float(hi[e]));
         }
+      }
 #pragma unroll
       for (int r = i; r < NT; ++r) {
         const uint32_t bits = (uint32_t)(s_anc[8 * r + gid] >> (8 * i + 2 * j));
         const uint32_t b0 = bits & 1 ? 0x3f800000u : 0u, b1 = bits & 2 ? 0x3f800000u : 0u;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma_raw(gam[r][m], hi[m][0], hi[m][1], hi[m][2], hi[m][3], b0, b1);
-          mma_raw(X3 ? low[X3 ? r : 0][m] : gam[r][m], lo[m][0], lo[m][1], lo[m][2], lo[m][3], b0, b1);
-          if (X3) mma_raw(low[X3 ? r : 0][m], lo2[m][0], lo2[m][1], lo2[m][2], lo2[m][3], b0, b1);
-        }
+        mma_raw(gam[r], hi[0], hi[1], hi[2], hi[3], b0, b1);
+        mma_raw(X3 ? low[X3 ? r : 0] : gam[r], lo[0], lo[1], lo[2], lo[3], b0, b1);
+        if (X3) mma_raw(low[X3 ? r : 0], lo2[0], lo2[1], lo2[2], lo2[3], b0, b1);
       }
     }
 #pragma unroll
@@ -336,20 +342,21 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       if (i >= tiles) break;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int t = 8 * i + 2 * j + e;
-        float kv[E], qv[E], kh[E];
-#pragma unroll
-        for (int c = 0; c < E; ++c) kv[c] = qv[c] = 0.f;
-        if (s_anc[t] != 0) {
-          const int64_t at = (row0 + (int64_t)t * H) * DK + c0;
-          load_row<E>(k + at, kv);
-          load_row<E>(q + at, qv);
+        const int t = place(i, e);
+        Pair<TIn> yk, yq;
+        if (AHEAD) {
+          yk = rk[AHEAD ? 2 * i + e : 0];
+          yq = rq[AHEAD ? 2 * i + e : 0];
+        } else if (s_anc[t] != 0) {
+          yk.load(k + at0 + t * step);
+          yq.load(q + at0 + t * step);
         }
+        float kv[E] = {yk.get().x, yk.get().y}, qv[E] = {yq.get().x, yq.get().y}, kh[E];
 #pragma unroll
         for (int c = 0; c < E; ++c) {
-          float G = gam[i][c >> 1][2 * (c & 1) + e], down, inv;
+          float G = gam[i][2 * c + e], down, inv;
           if (X3) {
-            const float b = low[X3 ? i : 0][c >> 1][2 * (c & 1) + e];
+            const float b = low[X3 ? i : 0][2 * c + e];
             const float sum = G + b, rest = b - (sum - G);
             G = sum;
             down = expf(G);
@@ -366,33 +373,26 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
           wide |= !(fabsf(kh[c]) < kFactorLimit) || !(fabsf(G) <= kGamLimit);
         }
         const int at = t * DK + ((((c0 >> 2) ^ swizzle(t)) << 2) | (c0 & 3));
-        store_row<E>(s_kt + at, kv);
-        store_row<E>(s_qt + at, qv);
-        store_row<E>(s_kh + at, kh);
+        store_pair(s_kt + at, kv[0], kv[1]);
+        store_pair(s_qt + at, qv[0], qv[1]);
+        store_pair(s_kh + at, kh[0], kh[1]);
       }
     }
   }
 
   // ---- -V, transposed: what the products below are added to (columns x places) ----
-  float vn[NT][MT][4];
-  {
-    const TIn *vp = v + row0 * DV + col;
+  float vn[NT][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = 8 * i + 2 * j + e;
-        float x[E];
-#pragma unroll
-        for (int c = 0; c < E; ++c) x[c] = 0.f;
-        if (s_anc[t] != 0) load_row<E>(vp + (int64_t)t * H * DV, x);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          vn[i][m][e] = -x[2 * m];
-          vn[i][m][2 + e] = -x[2 * m + 1];
-        }
-      }
-  }
+    for (int e = 0; e < 2; ++e) {
+      const int t = place(i, e);
+      Pair<TIn> y;
+      if (AHEAD) y = rv[AHEAD ? 2 * i + e : 0];
+      else if (s_anc[t] != 0) y.load(vp + (int64_t)t * H * DV);
+      vn[i][e] = -y.get().x;
+      vn[i][2 + e] = -y.get().y;
+    }
   wide = __syncthreads_or(wide);
 
   // Where this lane's 16-byte units of channels 16 a + 4 j lie in a row 8 i + gid.
@@ -497,13 +497,11 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   }
 
   // ---- Kt S0 - V and Qt S0, transposed, in one pass over the state ----
-  float o[NT][MT][4];
+  float o[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][m][e] = 0.f;
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
   for (int a = 0; a < DK / 16; ++a) {
 #pragma unroll
@@ -515,54 +513,43 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       if (i >= tiles) break;
       const float4 x = unit_at(s_kt, i, a), y = unit_at(s_qt, i, a);
       const Op<X3> x0(x.x), x1(x.y), x2(x.z), x3(x.w), y0(y.x), y1(y.y), y2(y.z), y3(y.w);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const Op<X3> a0(s0[4 * a][2 * m]), a1(s0[4 * a][2 * m + 1]), a2(s0[4 * a + 1][2 * m]),
-            a3(s0[4 * a + 1][2 * m + 1]);
-        mma<X3>(vn[i][m], a0, a1, a2, a3, x0, x1);
-        mma<X3>(o[i][m], a0, a1, a2, a3, y0, y1);
-        const Op<X3> d0(s0[4 * a + 2][2 * m]), d1(s0[4 * a + 2][2 * m + 1]),
-            d2(s0[4 * a + 3][2 * m]), d3(s0[4 * a + 3][2 * m + 1]);
-        mma<X3>(vn[i][m], d0, d1, d2, d3, x2, x3);
-        mma<X3>(o[i][m], d0, d1, d2, d3, y2, y3);
-      }
+      const Op<X3> a0(s0[4 * a][0]), a1(s0[4 * a][1]), a2(s0[4 * a + 1][0]), a3(s0[4 * a + 1][1]);
+      mma<X3>(vn[i], a0, a1, a2, a3, x0, x1);
+      mma<X3>(o[i], a0, a1, a2, a3, y0, y1);
+      const Op<X3> d0(s0[4 * a + 2][0]), d1(s0[4 * a + 2][1]), d2(s0[4 * a + 3][0]),
+          d3(s0[4 * a + 3][1]);
+      mma<X3>(vn[i], d0, d1, d2, d3, x2, x3);
+      mma<X3>(o[i], d0, d1, d2, d3, y2, y3);
     }
   }
   __syncthreads();   // the blocks' inverses
 
   // acc += x (rows of W)^T for one tile of places: W[8 r + gid][8 s + 2 j, + 1]
-  const auto apply = [&](float (&acc)[MT][4], const float (&x)[MT][4], const float *W) {
+  const auto apply = [&](float (&acc)[4], const float (&x)[4], const float *W) {
     const float2 w = *reinterpret_cast<const float2 *>(W);
-    const Op<X3> b0(w.x), b1(w.y);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-      mma<X3>(acc[m], Op<X3>(x[m][0]), Op<X3>(x[m][2]), Op<X3>(x[m][1]), Op<X3>(x[m][3]), b0, b1);
+    mma<X3>(acc, Op<X3>(x[0]), Op<X3>(x[2]), Op<X3>(x[1]), Op<X3>(x[3]), Op<X3>(w.x), Op<X3>(w.y));
   };
 
   // ---- (I + L) Vn = beta (V - Kt S0), block by block ----
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     if (BT * b >= tiles) break;
-    float r[BT][MT][4];
+    float r[BT][4];
 #pragma unroll
     for (int i = 0; i < BT; ++i) {
-      const float2 bt = *reinterpret_cast<const float2 *>(s_beta + 8 * (BT * b + i) + 2 * j);
+      const float2 bt2 = *reinterpret_cast<const float2 *>(s_beta + 8 * (BT * b + i) + 2 * j);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          r[i][m][e] = -(e & 1 ? bt.y : bt.x) * vn[BT * b + i][m][e];
-          vn[BT * b + i][m][e] = 0.f;
-        }
+      for (int e = 0; e < 4; ++e) {
+        r[i][e] = -(e & 1 ? bt2.y : bt2.x) * vn[BT * b + i][e];
+        vn[BT * b + i][e] = 0.f;
+      }
       if (BT * b + i < tiles) {
 #pragma unroll
         for (int s = 0; s < BT * b; ++s)
           apply(r[i], vn[s], s_L + (8 * (BT * b + i) + gid) * LDT + 8 * s + 2 * j);
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[i][m][e] = operand<X3>(r[i][m][e]);
+      for (int e = 0; e < 4; ++e) r[i][e] = operand<X3>(r[i][e]);
     }
 #pragma unroll
     for (int i = 0; i < BT; ++i) {
@@ -570,9 +557,7 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       for (int s = 0; s <= i; ++s)
         apply(vn[BT * b + i], r[s], s_M + (8 * (BT * b + i) + gid) * LDB + 8 * s + 2 * j);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) vn[BT * b + i][m][e] = operand<X3>(vn[BT * b + i][m][e]);
+      for (int e = 0; e < 4; ++e) vn[BT * b + i][e] = operand<X3>(vn[BT * b + i][e]);
     }
   }
 
@@ -586,16 +571,10 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int t = 8 * i + 2 * j + e;
+      const int t = place(i, e);
       if (t < T) {
         const bool live = s_anc[t] != 0;
-        float x[E];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          x[2 * m] = live ? o[i][m][e] : 0.f;
-          x[2 * m + 1] = live ? o[i][m][2 + e] : 0.f;
-        }
-        store_row<E>(op + (int64_t)t * H * DV, x);
+        store_pair(op + (int64_t)t * H * DV, live ? o[i][e] : 0.f, live ? o[i][2 + e] : 0.f);
       }
     }
   }
@@ -635,12 +614,13 @@ cudaError_t launch_decode_tree_t(int dk, int dv, const void *q, const void *k, c
                                  const float *g, const float *beta, const float *state,
                                  const int32_t *parents, void *out, int T, int64_t units, int H,
                                  cudaStream_t stream) {
-#define KDA_DT(DK_, DV_)      \
-  if (dk == DK_ && dv == DV_) \
+#define KDA_DT(DK_, DV_)                                                                          \
+  if (dk == DK_ && dv == DV_)                                                                     \
     return launch_d<DK_, DV_, TIn>(q, k, v, g, beta, state, parents, out, T, units, H, stream);
   KDA_DT(32, 32) KDA_DT(32, 64) KDA_DT(32, 128)
   KDA_DT(64, 32) KDA_DT(64, 64) KDA_DT(64, 128)
-  KDA_DT(128, 32) KDA_DT(128, 64) KDA_DT(128, 128)
+  KDA_DT(128, 32) KDA_DT(128, 64)
+  if constexpr (sizeof(TIn) == 4) KDA_DT(128, 128)   // BF16: the tensor-memory kernel
 #undef KDA_DT
   return cudaErrorInvalidValue;
 }
