@@ -121,9 +121,11 @@ template <> struct MaskOf<8> { using T = unsigned long long; };
 template <int DK, int DV, int NT, typename TIn> struct TreeCfg {
   static constexpr bool X3 = sizeof(TIn) == 4;
   static constexpr int WARPS = DV / 16;             // 16 value columns each, two per lane
-  // Rows are loaded into registers as soon as the paths are known, all at once, as long
-  // as there are registers for them.
-  static constexpr bool AHEAD = NT <= 4;
+  // Rows are loaded into registers as soon as the paths are known, all at once (512 x 32
+  // heads x 16 places of D = 64, BF16: 147 us, 223 when they are loaded where they are
+  // used; 128 x 32 x 61 places: 218 and 396), except where the registers cost the second
+  // CTA of an SM (FP32, 256 x 32 x 30 places, D = 64/128: 629 us, 577 without).
+  static constexpr bool AHEAD = !(X3 && NT == 4 && WARPS == 8 && DK < 128);
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int T8 = 8 * NT;
   static constexpr int NB = NT < 2 ? 1 : NT / 2;    // diagonal blocks
