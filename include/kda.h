@@ -264,9 +264,11 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const f
  *   q, k, g : [N, nodes_per_seq, H, D_k]   v, out : [N, nodes_per_seq, H, D_v]
  *   beta    : [N, nodes_per_seq, H]         state  : [N, H, D_k, D_v] FP32
  *   parents : device int32[N, nodes_per_seq] or NULL
- * Rows of out at empty places are zero; what q, k, v, g and
- * beta hold there does not matter.  FP32 inputs give FP32
- * accuracy; BF16 inputs run the products in TF32, below the rounding of out.
+ * Rows of out at empty places are zero; what q, k, v, g and beta hold there does
+ * not matter.  FP32 inputs give FP32 accuracy; BF16 inputs run the products in
+ * TF32, below the rounding of out.  BF16 with D_k = D_v = 128 runs on the tensor
+ * cores with the state in tensor memory (its waits are bounded, dev_status tells
+ * of one that ran out); other shapes run warp-level tensor products.
  *
  * kda_tree_commit: state_out = the state after place accept_node[n], by the
  * recurrence in FP32 along its path.  A value outside [0, nodes_per_seq), or an
@@ -275,7 +277,12 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const f
  *   accept_node : device int32[N]; other arguments as above.
  *
  * shape->total_tokens must equal N * nodes_per_seq; 1 <= nodes_per_seq <= 64;
- * shape->chunk and shape->dev_status are ignored.
+ * shape->chunk is ignored, and so is shape->dev_status by the commit.
+ *
+ * The calls of this section, of verification and of the state cache may start
+ * before the one ahead of them in the stream has ended, and then wait for it
+ * before they touch memory (programmatic dependent launch); what a stream's order
+ * promises is unchanged.
  */
 kda_status kda_decode_tree(const void *q, const void *k, const void *v, const float *g,
                            const float *beta, const float *state, const int32_t *parents,
@@ -314,8 +321,9 @@ kda_status kda_tree_commit(const void *k, const void *v, const float *g, const f
  *   out_tokens   : int32[N, nodes_per_seq + 1]: the accepted tokens, the drawn
  *                  one (-1 if its row holds no probability at all), then -1.
  * Probabilities are FP32 or BF16 (prob_dtype, a kda_dtype), non-negative and
- * finite; rows need no more alignment than their elements (rows of a multiple
- * of 16 bytes are read fastest).  All pointers are device pointers.
+ * finite (whatever is not above zero counts as zero); rows need no more alignment
+ * than their elements (rows of a multiple of 16 bytes are read fastest).  All
+ * pointers are device pointers.
  * vocab <= 2^30, num_seqs <= 2^27, 1 <= nodes_per_seq <= 64.
  */
 kda_status kda_verify_tree(const void *target_probs, const void *draft_probs,

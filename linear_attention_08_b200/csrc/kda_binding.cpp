@@ -97,17 +97,21 @@ kda_shape make_shape(int64_t n, int64_t tokens, int64_t h, int64_t dk, int64_t d
 }
 
 // The arguments' device made current, and the stream: an address, or None for that
-// device's current one.
+// device's current one.  A stream that is given is current while outputs are made, so
+// that their memory is that stream's and is not handed on while it is still written.
 struct Where {
   c10::cuda::CUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard on;
   kda_stream_t stream;
   Where(c10::Device device, PyObject *s) : guard(device) {
     if (s == Py_None) {
       stream = reinterpret_cast<kda_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
-    } else {
-      stream = static_cast<kda_stream_t>(PyLong_AsVoidPtr(s));
-      if (PyErr_Occurred()) throw Refused{};
+      return;
     }
+    stream = static_cast<kda_stream_t>(PyLong_AsVoidPtr(s));
+    if (PyErr_Occurred()) throw Refused{};
+    on.reset_stream(stream ? c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), device.index())
+                           : c10::cuda::getDefaultCUDAStream(device.index()));
   }
 };
 
@@ -153,14 +157,15 @@ Tree tree(PyObject *ok, PyObject *ov, PyObject *og, PyObject *ob, PyObject *os, 
   return {N, T, H, Dk, Dv, dt, dev, k, v, g, b, s, p};
 }
 
-// (q, k, v, g, beta, state, parents, out, stream) -> (status, out)
+// (q, k, v, g, beta, state, parents, out, stream, dev_status) -> (status, out)
 PyObject *decode_tree(PyObject *const *a, Py_ssize_t n) {
-  arguments(n, 9);
+  arguments(n, 10);
   const Tree t = tree(a[1], a[2], a[3], a[4], a[5], a[6]);
   const Tensor &q = want("q", a[0], t.k.sizes(), t.dtype, t.device);
   const Where at(t.device, a[8]);
   const Tensor out = want_or_new("out", a[7], t.v.sizes(), t.dtype, t.device);
-  const kda_shape s = make_shape(t.N, t.N * t.T, t.H, t.Dk, t.Dv, float_code("q/k/v", t.k));
+  kda_shape s = make_shape(t.N, t.N * t.T, t.H, t.Dk, t.Dv, float_code("q/k/v", t.k));
+  if (a[9] != Py_None) s.dev_status = address<int32_t>(want("dev_status", a[9], {1}, at::kInt, t.device));
   const int32_t nodes = to_int32("the number of places", t.T);
   const int st = call([&] {
     return kda_decode_tree(q.data_ptr(), t.k.data_ptr(), t.v.data_ptr(), address<float>(t.g),

@@ -372,16 +372,19 @@ def _raw(stream):
     return None if stream is None else stream.cuda_stream
 
 
-def kda_decode_tree(q, k, v, g, beta, state, *, parents=None, out=None, stream=None):
+def kda_decode_tree(q, k, v, g, beta, state, *, parents=None, out=None, dev_status=None,
+                    stream=None):
     """Outputs of a tree of drafted tokens over each sequence's state (see
     kda_decode_tree in include/kda.h): q, k, g [N, T, H, Dk]; v [N, T, H, Dv];
     beta [N, T, H]; state [N, H, Dk, Dv] FP32, only read; parents [N, T] int32
     (place of the token before, -1 for the state, -2 for an empty place) or None
-    for chains; T <= 64.  Returns out [N, T, H, Dv], zero at empty places.
+    for chains; T <= 64; dev_status [1] int32 or None.  Returns out [N, T, H, Dv],
+    zero at empty places.
 
     This call and the ones below run on the arguments' device, on ``stream`` or
-    that device's current stream."""
-    st, out = (_native_module or _native()).decode_tree(q, k, v, g, beta, state, parents, out, _raw(stream))
+    that device's current stream; outputs they make are memory of that stream."""
+    st, out = (_native_module or _native()).decode_tree(q, k, v, g, beta, state, parents, out, _raw(stream),
+                                                       dev_status)
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_tree")
     return out
