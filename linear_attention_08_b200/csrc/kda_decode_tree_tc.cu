@@ -228,7 +228,6 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be uniform
   const auto bar_at = [&](int b) { return sb + C::BAR + 8 * b; };
 
-  launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i)   // rows: a lane's copies each, and the masks
       mbar_init(bars + i, i == kEmptyQkg || i == kEmptyV || i == kEmptyS ? C::WORKERS / 32
@@ -238,12 +237,15 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     *s_quit = 0;
     s_wide[0] = s_wide[1] = 0;
   }
+  // Tensor memory is taken after the kernel ahead has ended, and before the next one may
+  // start: a block that held some while it waits could keep it from the one it waits for.
+  wait_for_inputs();
   if (warp == 0) tc::tmem_alloc(sb + C::SLOT, C::COLS);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  launch_dependents();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sp + C::SLOT), 0);
-  wait_for_inputs();
 
   if (warp == C::WORKERS / 32) {
     // ------------------------------------------------------------ producer
@@ -537,7 +539,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         else tc::fence_smem_to_async();
         tc::fence_before_sync();
         if (bar_or<C::WORKERS>(bad)) { aborted = true; break; }
-        // Two threads issue: it takes one about 70 cycles per product.
+        // Two warps issue, one product each.
         if (warp == 1 && elect_one()) {
           tc::fence_after_sync();
 #pragma unroll

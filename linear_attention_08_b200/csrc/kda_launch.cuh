@@ -2,7 +2,7 @@
 // (programmatic dependent launch), for kernels that take a few microseconds.
 //
 // Such a kernel's blocks are started as soon as every block of the kernel ahead has
-// called launch_dependents() or ended; they set up their shared and tensor memory, and
+// called launch_dependents() or ended; they set up their shared memory, and
 // wait_for_inputs() returns once the kernel ahead has completed and its writes are
 // visible.  No global memory is touched before that.  A kernel ahead that does not call
 // launch_dependents() has the usual order.  One user's calls in a row: tree decode 8.2 ->
