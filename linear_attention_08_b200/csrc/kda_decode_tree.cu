@@ -18,16 +18,18 @@
 // Layout: one CTA per (sequence, head).  Everything is computed transposed,
 // O^T = S0^T Qt^T + Vn^T P^T, with value columns as the rows of m16n8k8 products:
 //   - the A operand S0^T comes straight from the row-major FP32 state in HBM into
-//     the registers of the warp that owns the columns (a lane reads float4s of
-//     four columns; which tile row a column is and which k index a state row is
+//     the registers of the warp that owns the columns (a lane reads pairs of
+//     columns; which tile row a column is and which k index a state row is
 //     are free choices), no shared memory, no transposition;
 //   - the accumulators of Kt S0 have the layout of an A operand, so V - Kt S0, Vn
 //     and the outputs stay in registers from the first product to the store.
-// Shared memory holds the token rows (Kt, Qt, Kh) and the T x T matrices.  The
-// contractions are small and the state crosses HBM once, so the kernel is bound
-// by memory; the warp-level products need no tensor-memory round trip per unit
-// and no staging of the state, which the 5th-generation tile products (operands
-// in shared memory, accumulators in tensor memory) would.
+// Shared memory holds the token rows (Kt, Qt, Kh) and the T x T matrices.  BF16 with
+// D_k = D_v = 128 runs the tensor-memory kernel of kda_decode_tree_tc.cu, which needs
+// value columns for all 128 lanes of an accumulator; this one serves the other head
+// sizes, and FP32, whose three products per product the warp-level instructions take
+// with operands split in registers.  It is bound by issue slots and by the round trips
+// to memory (parents, then all rows at once): 512 x 32 heads x 16 places of D = 64 in
+// BF16 take 147 us against 72 at the copy rate, of D = 128 in FP32 703 against 267.
 //
 // Arithmetic: TF32 products with FP32 accumulation for BF16 inputs (operands are
 // rounded to nearest, 2^-12 of a value, against 2^-9 when out is rounded).  FP32
