@@ -32,7 +32,8 @@
 // BF16 take 147 us against 72 at the copy rate, of D = 128 in FP32 703 against 267.
 //
 // Arithmetic: TF32 products with FP32 accumulation for BF16 inputs (operands are
-// rounded to nearest, 2^-12 of a value, against 2^-9 when out is rounded).  FP32
+// rounded to about the nearest, 2^-11.7 of a value rms, against 2^-9 when out is
+// rounded).  FP32
 // inputs split each operand in two TF32 terms and add three products, and carry
 // Gam as an unevaluated sum of two FP32 numbers, for FP32 accuracy.
 #include "kda_common.cuh"
@@ -44,24 +45,23 @@ namespace {
 constexpr float kGamLimit = 80.f;
 constexpr float kFactorLimit = 1e36f;
 
-__device__ __forceinline__ uint32_t tf32_rn(float x) {
+// Rounded by the conversion instruction.
+__device__ __forceinline__ float rn_tf32(float x) {
   uint32_t r;
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
+  return __uint_as_float(r);
 }
-
 // An operand of the products.  For X3 it is an FP32 value, split into two TF32
-// terms where it is used; otherwise it is a value rounded to TF32 when it was made
-// (operand<X3>), whose bits go in as they are.
-template <bool X3> __device__ __forceinline__ float operand(float x) {
-  return X3 ? x : __uint_as_float(tf32_rn(x));
-}
+// terms where it is used; otherwise it is a value made ready for the cut to TF32 when it
+// was made (operand<X3>), whose bits go in as they are.
+template <bool X3> __device__ __forceinline__ float operand(float x) { return X3 ? x : to_tf32(x); }
 template <bool X3> struct Op {
   uint32_t hi, lo;
   __device__ __forceinline__ explicit Op(float x) {
     if (X3) {
-      hi = tf32_rn(x);
-      lo = tf32_rn(x - __uint_as_float(hi));
+      const float h = cut_tf32(x);
+      hi = __float_as_uint(h);
+      lo = __float_as_uint(x - h);      // exact; cut in the product, 2^-21 of x
     } else {
       hi = __float_as_uint(x);
     }
@@ -325,11 +325,13 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
           const float r = rintf(y * 8.f) * 0.125f;
           hi[e] = __float_as_uint(r);
           y -= r;
-          lo[e] = tf32_rn(y);
-          lo2[e] = tf32_rn(y - __uint_as_float(lo[e]));
+          const float l = cut_tf32(y);
+          lo[e] = __float_as_uint(l);
+          lo2[e] = __float_as_uint(y - l);
         } else {
-          hi[e] = tf32_rn(y);
-          lo[e] = tf32_rn(y - __uint_as_float(hi[e]));
+          const float h = cut_tf32(y);
+          hi[e] = __float_as_uint(h);
+          lo[e] = __float_as_uint(y - h);
         }
       }
 #pragma unroll
@@ -511,7 +513,13 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int e = 0; e < E; ++e) s0[4 * a + m][e] = operand<X3>(s0[4 * a + m][e]);
+      for (int e = 0; e < E; ++e) {
+        // The conversion instruction is slower than the product of operand(), but with 64
+        // elements per lane the code around it comes out faster (512 x 32 heads x 16
+        // places, BF16: D = 128/64 243 us against 310; D = 64/128 309 against 252).
+        float &x = s0[4 * a + m][e];
+        x = !X3 && DK == 128 ? rn_tf32(x) : operand<X3>(x);
+      }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       if (i >= tiles) break;

@@ -153,19 +153,6 @@ __device__ __forceinline__ void mma_tf32_ts(uint32_t d, uint32_t a, uint64_t b, 
       : "memory");
 }
 
-// The products take the upper 19 bits of an operand.  A factor of 1 + 2^-11.5 ahead of
-// that makes the cut a rounding: it adds 0.35 to 0.71 units in the last place of TF32, so
-// that the error is 0.71 units at most and has no bias (rms 0.31 units, 0.29 for rounding
-// to nearest), numbers that TF32 holds stay as they are, and so do infinities and NaN,
-// which adding half a unit to the bits would lose; the conversion instruction is too slow
-// (272 us instead of 236 for 512 x 32 heads x 16 places).
-constexpr float kTf32 = 1.00034526698f, kLog2Tf32 = 4.98029e-4f;
-__device__ __forceinline__ float to_tf32(float x) { return x * kTf32; }
-// The same with the cut made, for values that are used outside the products, too.
-__device__ __forceinline__ float cut_tf32(float x) {
-  return __uint_as_float(__float_as_uint(x * kTf32) & 0xffffe000u);
-}
-
 // Descriptor of K-step s (8 columns) of a K-major tile from the one of its first step:
 // the steps lie at fixed distances.
 __device__ __forceinline__ uint64_t step_desc(uint64_t first, int rows, int s) {
