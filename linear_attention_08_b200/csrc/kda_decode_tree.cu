@@ -29,7 +29,7 @@
 // sizes, and FP32, whose three products per product the warp-level instructions take
 // with operands split in registers.  It is bound by issue slots and by the round trips
 // to memory (parents, then all rows at once): 512 x 32 heads x 16 places of D = 64 in
-// BF16 take 147 us against 72 at the copy rate, of D = 128 in FP32 703 against 267.
+// BF16 take 132 us against 72 at the copy rate, of D = 128 in FP32 618 against 267.
 //
 // Arithmetic: TF32 products with FP32 accumulation for BF16 inputs (operands are
 // rounded to about the nearest, 2^-11.7 of a value rms, against 2^-9 when out is
@@ -87,6 +87,22 @@ __device__ __forceinline__ void mma(float (&c)[4], const Op<X3> &a0, const Op<X3
   mma_raw(c, a0.hi, a1.hi, a2.hi, a3.hi, b0.hi, b1.hi);
 }
 
+// What a few products add to an accumulator.  The tensor cores cut, not round, what they
+// add to their accumulators (over 48 products of one sum that was 1.6e-6 of the outputs),
+// so for X3 a short sum starts from zero and is added by an FP32 addition: 2.0e-7, for 4 %
+// of the time.
+template <bool X3> struct Sum {
+  float c[4];
+  __device__ __forceinline__ explicit Sum(const float (&acc)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = X3 ? 0.f : acc[e];
+  }
+  __device__ __forceinline__ void add_to(float (&acc)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = X3 ? acc[e] + c[e] : c[e];
+  }
+};
+
 // Token rows lie in shared memory without padding, in 16-byte units whose low
 // three index bits are exclusive-ored with this function of the row: reads of
 // units 4 a + j of rows 8 i + gid, and writes of unit gid (or half a unit) of rows
@@ -124,7 +140,7 @@ template <int DK, int DV, int NT, typename TIn> struct TreeCfg {
   static constexpr bool X3 = sizeof(TIn) == 4;
   static constexpr int WARPS = DV / 16;             // 16 value columns each, two per lane
   // Rows are loaded into registers as soon as the paths are known, all at once (512 x 32
-  // heads x 16 places of D = 64, BF16: 147 us, 223 when they are loaded where they are
+  // heads x 16 places of D = 64, BF16: 147 us, 223 when they were loaded where they are
   // used; 128 x 32 x 61 places: 218 and 396), except where the registers cost the second
   // CTA of an SM (FP32, 256 x 32 x 30 places, D = 64/128: 629 us, 577 without).
   static constexpr bool AHEAD = !(X3 && NT == 4 && WARPS == 8 && DK < 128);
@@ -422,8 +438,11 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i) {
         const float4 x = unit_at(s_kt, a, i), y = unit_at(s_qt, a, i), z = unit_at(s_kh, b, i);
-        mma<X3>(c, Op<X3>(x.x), Op<X3>(y.x), Op<X3>(x.y), Op<X3>(y.y), Op<X3>(z.x), Op<X3>(z.y));
-        mma<X3>(c2, Op<X3>(x.z), Op<X3>(y.z), Op<X3>(x.w), Op<X3>(y.w), Op<X3>(z.z), Op<X3>(z.w));
+        Sum<X3> s1(c), s2(c2);
+        mma<X3>(s1.c, Op<X3>(x.x), Op<X3>(y.x), Op<X3>(x.y), Op<X3>(y.y), Op<X3>(z.x), Op<X3>(z.y));
+        mma<X3>(s2.c, Op<X3>(x.z), Op<X3>(y.z), Op<X3>(x.w), Op<X3>(y.w), Op<X3>(z.z), Op<X3>(z.w));
+        s1.add_to(c);
+        s2.add_to(c2);
       }
       const int t = 8 * a + gid;
       const Mask anc = s_anc[t];
@@ -526,12 +545,15 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       const float4 x = unit_at(s_kt, i, a), y = unit_at(s_qt, i, a);
       const Op<X3> x0(x.x), x1(x.y), x2(x.z), x3(x.w), y0(y.x), y1(y.y), y2(y.z), y3(y.w);
       const Op<X3> a0(s0[4 * a][0]), a1(s0[4 * a][1]), a2(s0[4 * a + 1][0]), a3(s0[4 * a + 1][1]);
-      mma<X3>(vn[i], a0, a1, a2, a3, x0, x1);
-      mma<X3>(o[i], a0, a1, a2, a3, y0, y1);
       const Op<X3> d0(s0[4 * a + 2][0]), d1(s0[4 * a + 2][1]), d2(s0[4 * a + 3][0]),
           d3(s0[4 * a + 3][1]);
-      mma<X3>(vn[i], d0, d1, d2, d3, x2, x3);
-      mma<X3>(o[i], d0, d1, d2, d3, y2, y3);
+      Sum<X3> sv(vn[i]), so(o[i]);
+      mma<X3>(sv.c, a0, a1, a2, a3, x0, x1);
+      mma<X3>(so.c, a0, a1, a2, a3, y0, y1);
+      mma<X3>(sv.c, d0, d1, d2, d3, x2, x3);
+      mma<X3>(so.c, d0, d1, d2, d3, y2, y3);
+      sv.add_to(vn[i]);
+      so.add_to(o[i]);
     }
   }
   __syncthreads();   // the blocks' inverses
@@ -539,7 +561,9 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   // acc += x (rows of W)^T for one tile of places: W[8 r + gid][8 s + 2 j, + 1]
   const auto apply = [&](float (&acc)[4], const float (&x)[4], const float *W) {
     const float2 w = *reinterpret_cast<const float2 *>(W);
-    mma<X3>(acc, Op<X3>(x[0]), Op<X3>(x[2]), Op<X3>(x[1]), Op<X3>(x[3]), Op<X3>(w.x), Op<X3>(w.y));
+    Sum<X3> sum(acc);
+    mma<X3>(sum.c, Op<X3>(x[0]), Op<X3>(x[2]), Op<X3>(x[1]), Op<X3>(x[3]), Op<X3>(w.x), Op<X3>(w.y));
+    sum.add_to(acc);
   };
 
   // ---- (I + L) Vn = beta (V - Kt S0), block by block ----
