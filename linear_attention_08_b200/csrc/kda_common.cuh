@@ -32,6 +32,12 @@ __device__ __forceinline__ float cut_tf32(float x) {
   return __uint_as_float(__float_as_uint(x * kTf32) & 0xffffe000u);
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Read-only, streamed once: keep it out of L1.
 template <typename T> __device__ __forceinline__ float ldg_stream(const T *p) {
   return to_f32(__ldcs(p));

@@ -43,7 +43,15 @@ namespace kda {
 namespace {
 
 constexpr float kGamLimit = 80.f;
-constexpr float kFactorLimit = 1e36f;
+constexpr float kFactorLimit = 0x1p120f;
+// At Gam = -80 an element of Kt is 1.8e-35 of k's: a subnormal number for small rows of q and
+// k, and for FP32 inputs its second TF32 term, 2^-12 of it, is one for most (16 places with
+// gates of -5, q of size 10^-2: 1e-4 off).  So Kh is held divided by a power of two, and
+// - FP32: Kt and Qt enter L and P times that, by the split in two terms; terms keep 2^-24 of an
+//   element down to 2^-26, and rows too large for it go pair by pair;
+// - BF16: Kt and Qt are held times it, V and P as well, and divided again on the way to Vn and
+//   out (states or outputs above 10^31 overflow).
+template <bool X3> __device__ constexpr float lift() { return X3 ? 0x1p40f : 0x1p24f; }
 
 // Rounded by the conversion instruction.
 __device__ __forceinline__ float rn_tf32(float x) {
@@ -65,6 +73,16 @@ template <bool X3> struct Op {
     } else {
       hi = __float_as_uint(x);
     }
+  }
+  // Of an element of Kt or Qt, times the lift (BF16: it is held so).
+  static __device__ __forceinline__ Op lifted(float x) {
+    Op r(x);
+    if (X3) {
+      const float h = __uint_as_float(__float_as_uint(x * (kTf32 * lift<X3>())) & 0xffffe000u);
+      r.hi = __float_as_uint(h);
+      r.lo = __float_as_uint(fmaf(x, lift<X3>(), -h));
+    }
+    return r;
   }
 };
 
@@ -168,6 +186,7 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   using Cfg = TreeCfg<DK, DV, NT, TIn>;
   using Mask = typename MaskOf<NT>::T;
   constexpr bool X3 = Cfg::X3;
+  constexpr float kHeld = X3 ? 1.f : lift<X3>();   // what Kt, Qt, V and P are held times
   constexpr int T8 = Cfg::T8, LDT = Cfg::LDT, E = 2;
   constexpr bool AHEAD = Cfg::AHEAD;
   constexpr int LDB = Cfg::LDB, BT = Cfg::BT, NB = Cfg::NB;
@@ -384,15 +403,17 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
             down = expf(G);
             down += down * rest;
             inv = expf(-G);
-            inv -= inv * rest;
-          } else {
-            down = __expf(G);
-            inv = __expf(-G);
+            inv = (inv - inv * rest) * (1.f / lift<X3>());
+          } else {                              // and made ready for the cut
+            down = __expf(G) * (kTf32 * lift<X3>());
+            inv = __expf(-G) * (kTf32 / lift<X3>());
           }
-          kh[c] = operand<X3>(kv[c] * inv);
-          kv[c] = operand<X3>(kv[c] * down);
-          qv[c] = operand<X3>(qv[c] * down);
-          wide |= !(fabsf(kh[c]) < kFactorLimit) || !(fabsf(G) <= kGamLimit);
+          kh[c] = kv[c] * inv;
+          float top = fabsf(kh[c]);
+          if (X3) top = fmaxf(top, fmaxf(fabsf(kv[c]), fabsf(qv[c])));
+          kv[c] *= down;
+          qv[c] *= down;
+          wide |= !(top < kFactorLimit / lift<X3>()) || !(fabsf(G) <= kGamLimit);
         }
         const int at = t * DK + ((((c0 >> 2) ^ swizzle(t)) << 2) | (c0 & 3));
         store_pair(s_kt + at, kv[0], kv[1]);
@@ -412,8 +433,8 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       Pair<TIn> y;
       if (AHEAD) y = rv[AHEAD ? 2 * i + e : 0];
       else if (s_anc[t] != 0) y.load(vp + (int64_t)t * H * DV);
-      vn[i][e] = -y.get().x;
-      vn[i][2 + e] = -y.get().y;
+      vn[i][e] = y.get().x * -kHeld;
+      vn[i][2 + e] = y.get().y * -kHeld;
     }
   wide = __syncthreads_or(wide);
 
@@ -425,7 +446,7 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
   // L as the diagonal blocks' inverses need it, -L as an operand elsewhere.
   const auto put = [&](int t, int s, float lt, float pt) {
     s_L[t * LDT + s] = t / (8 * BT) == s / (8 * BT) ? lt : operand<X3>(-lt);
-    s_P[t * LDT + s] = operand<X3>(pt);
+    s_P[t * LDT + s] = X3 ? pt : pt * (kTf32 * kHeld);
   };
 
   // ---- L and P: tile (a, b) of 8 x 8 places, rows Kt and Qt of one tile in one product ----
@@ -438,9 +459,10 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i) {
         const float4 x = unit_at(s_kt, a, i), y = unit_at(s_qt, a, i), z = unit_at(s_kh, b, i);
+        const auto up = [](float e) { return Op<X3>::lifted(e); };
         Sum<X3> s1(c), s2(c2);
-        mma<X3>(s1.c, Op<X3>(x.x), Op<X3>(y.x), Op<X3>(x.y), Op<X3>(y.y), Op<X3>(z.x), Op<X3>(z.y));
-        mma<X3>(s2.c, Op<X3>(x.z), Op<X3>(y.z), Op<X3>(x.w), Op<X3>(y.w), Op<X3>(z.z), Op<X3>(z.w));
+        mma<X3>(s1.c, up(x.x), up(y.x), up(x.y), up(y.y), Op<X3>(z.x), Op<X3>(z.y));
+        mma<X3>(s2.c, up(x.z), up(y.z), up(x.w), up(y.w), Op<X3>(z.z), Op<X3>(z.w));
         s1.add_to(c);
         s2.add_to(c2);
       }
@@ -573,10 +595,11 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
     float r[BT][4];
 #pragma unroll
     for (int i = 0; i < BT; ++i) {
-      const float2 bt2 = *reinterpret_cast<const float2 *>(s_beta + 8 * (BT * b + i) + 2 * j);
+      float2 bt2 = *reinterpret_cast<const float2 *>(s_beta + 8 * (BT * b + i) + 2 * j);
+      bt2 = make_float2(bt2.x * (-1.f / kHeld), bt2.y * (-1.f / kHeld));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        r[i][e] = -(e & 1 ? bt2.y : bt2.x) * vn[BT * b + i][e];
+        r[i][e] = (e & 1 ? bt2.y : bt2.x) * vn[BT * b + i][e];
         vn[BT * b + i][e] = 0.f;
       }
       if (BT * b + i < tiles) {
@@ -610,7 +633,8 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       const int t = place(i, e);
       if (t < T) {
         const bool live = s_anc[t] != 0;
-        store_pair(op + (int64_t)t * H * DV, live ? o[i][e] : 0.f, live ? o[i][2 + e] : 0.f);
+        store_pair(op + (int64_t)t * H * DV, live ? o[i][e] * (1.f / kHeld) : 0.f,
+                   live ? o[i][2 + e] * (1.f / kHeld) : 0.f);
       }
     }
   }

@@ -40,6 +40,11 @@ constexpr int kD = 128;
 constexpr int kBlk = 16;                  // tokens solved in registers at a time
 constexpr float kGamBound = 80.f;         // beyond: KK and P pair by pair
 constexpr float kFactorBound = 1e36f;
+// At Gam = -80 an element of Kt is 1.8e-35 of k's, and rows of q or k of size 10^-5 would be
+// subnormal numbers.  So X holds Kt and Qt times 2^24, Kh and S0^T are times 2^-24, and the
+// products come out as they are: exact, but for elements of S0 below 2^-102 and rows above
+// 10^31.
+constexpr float kLift = 24.f, kSink = 0x1p-24f;
 
 // TP: token places of the buffers.
 template <int TP> struct TreeTc {
@@ -174,12 +179,6 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r));
   return r != 0;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
 }
 
 // Barrier of the computing threads with a common "or".
@@ -443,7 +442,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           const int k0 = 32 * (b * C::WG + hw);
           float x[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = to_tf32(sf[(k0 + e) * kD]);
+          for (int e = 0; e < 32; ++e) x[e] = sf[(k0 + e) * kD] * (kTf32 * kSink);
           tc::tmem_st32(tl + C::S + (uint32_t)k0, x);
         }
         tc::tmem_wait_st();
@@ -511,9 +510,9 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
           for (int j = 0; j < kBlk; ++j) {
             if (j == kBlk / 2 && t0 + j >= last) break;   // (what the rows held is masked)
             const float kv = __bfloat162float(rk[(t0 + j) * kD]), qv = __bfloat162float(rq[(t0 + j) * kD]);
-            // powers of two, times kTf32
-            const float down = exp2_approx(fmaf(Gt[j], 1.44269504f, kLog2Tf32));
-            const float d = kv * exp2_approx(fmaf(Gt[j], -1.44269504f, kLog2Tf32));
+            // powers of two, times kTf32 and the lift
+            const float down = exp2_approx(fmaf(Gt[j], 1.44269504f, kLog2Tf32 + kLift));
+            const float d = kv * exp2_approx(fmaf(Gt[j], -1.44269504f, kLog2Tf32 - kLift));
             wide |= !(fabsf(Gt[j]) <= kGamBound && fabsf(d) < kFactorBound);
             const uint32_t at = (within ^ ((j & 7) << 4)) + j * 128;
             *reinterpret_cast<float *>(xt + at) = kv * down;
