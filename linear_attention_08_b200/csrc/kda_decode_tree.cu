@@ -364,6 +364,7 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
           lo[e] = __float_as_uint(l);
           lo2[e] = __float_as_uint(y - l);
         } else {
+          y = y < -1e5f ? -1e5f : y;            // finite: it meets zeros in the product
           const float h = cut_tf32(y);
           hi[e] = __float_as_uint(h);
           lo[e] = __float_as_uint(y - h);
