@@ -265,7 +265,10 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const f
  *   beta    : [N, nodes_per_seq, H]         state  : [N, H, D_k, D_v] FP32
  *   parents : device int32[N, nodes_per_seq] or NULL
  * Rows of out at empty places are zero; what q, k, v, g and beta hold there does
- * not matter.  FP32 inputs give FP32 accuracy; BF16 inputs run the products in
+ * not matter.  g may be -inf (alpha = 0).  Other numbers that are not finite are
+ * outside the preconditions: they leave the outputs of the tokens that follow
+ * them not finite, perhaps those of other branches of the same sequence and head,
+ * and no others.  FP32 inputs give FP32 accuracy; BF16 inputs run the products in
  * TF32, below the rounding of out.  BF16 with D_k = D_v = 128 runs on the tensor
  * cores with the state in tensor memory (its waits are bounded, dev_status tells
  * of one that ran out); other shapes run warp-level tensor products.

@@ -38,6 +38,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// The larger of two numbers, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Read-only, streamed once: keep it out of L1.
 template <typename T> __device__ __forceinline__ float ldg_stream(const T *p) {
   return to_f32(__ldcs(p));

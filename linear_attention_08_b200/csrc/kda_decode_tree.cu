@@ -356,7 +356,7 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       for (int e = 0; e < 4; ++e) {
         float y = x[e >> 1][e & 1];             // a0, a1: place 2 j; a2, a3: place 2 j + 1
         if (X3) {
-          y = fmaxf(y, -128.f);                 // exp(-128) is 0 in FP32 already
+          y = max_nan(y, -128.f);               // exp(-128) is 0 in FP32 already
           const float r = rintf(y * 8.f) * 0.125f;
           hi[e] = __float_as_uint(r);
           y -= r;
@@ -364,7 +364,7 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
           lo[e] = __float_as_uint(l);
           lo2[e] = __float_as_uint(y - l);
         } else {
-          y = y < -1e5f ? -1e5f : y;            // finite: it meets zeros in the product
+          y = max_nan(y, -1e5f);                // finite: it meets zeros in the product
           const float h = cut_tf32(y);
           hi[e] = __float_as_uint(h);
           lo[e] = __float_as_uint(y - h);

@@ -459,7 +459,8 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         float x[kBlk], y[kBlk];
 #pragma unroll
         for (int j = 0; j < kBlk; ++j) {
-          y[j] = fmaxf(rg[(kBlk * b + j) * kD], -1e5f);   // finite: it meets zeros in the product
+          // finite where it may be -inf: it meets zeros in the product
+          y[j] = max_nan(rg[(kBlk * b + j) * kD], -1e5f);
           x[j] = __uint_as_float((__float_as_uint(y[j]) + 0x1000u) & 0xffffe000u);
           y[j] -= x[j];
         }

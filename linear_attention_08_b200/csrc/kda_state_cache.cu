@@ -91,13 +91,6 @@ __device__ __forceinline__ uint32_t encode4(float4 x, float scale, const Factor 
   return scale > 0.f ? encode4_exact<E4M3>(x, scale) : 0u;   // false for a NaN scale too
 }
 
-// The larger of two magnitudes, NaN if one is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 template <bool E4M3> __device__ __forceinline__ float4 decode4(uint32_t c, float scale) {
   float4 x;
   if (E4M3) {

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import spec_ref as ref
-from test_gpu_tree_range import SHAPES, run
+from test_gpu_tree_range import ROWS, SHAPES, run
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,24 @@ def test_a_reset_by_an_infinite_gate(dtype, dims, T):
     out = ref.f64(run(d, parents))
     for n in range(2):
         assert np.linalg.norm(out[n] - want[n]) <= TOL[dtype] * np.linalg.norm(want[n])
+
+
+@pytest.mark.parametrize("dtype,dims", SHAPES)
+@pytest.mark.parametrize("T", [11, 27, 59])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("where", ROWS)
+def test_no_number_stays_none_on_its_path(dtype, dims, T, where, bad):
+    """NaN or infinity in one row of one place: outputs that are no numbers by the recurrence
+    are none here, and other sequences and heads are as the recurrence has them."""
+    d = ref.make_tokens(2, T, 2, *dims, dtype, seed=95)
+    parents = torch.tensor([TREE + list(range(10, T - 1))] * 2, dtype=torch.int32)
+    for n, t, h in ((0, 2, 1), (1, 5, 0)):
+        d[where][(n, t, h) + ((9,) if where != "beta" else ())] = bad
+    with np.errstate(all="ignore"):
+        want, _, _ = ref.tree(d, parents)
+    out = ref.f64(run(d, parents))
+    fine = np.isfinite(want)
+    assert not fine.all() and not np.isfinite(out[~fine]).any()
+    for n, h in ((0, 0), (1, 1)):
+        a, b = out[n, :, h], want[n, :, h]
+        assert np.linalg.norm(a - b) <= TOL[dtype] * np.linalg.norm(b)
