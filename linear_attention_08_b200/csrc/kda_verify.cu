@@ -278,7 +278,8 @@ verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
     s_tok[tid] = x;
     s_par[tid] = up;
     s_p[tid] = up >= -1 && in ? to_f32(trow[(int64_t)(up + 1) * vocab + x]) : 0.f;
-    s_d[tid] = drow && up >= -1 && in ? to_f32(drow[(int64_t)(up + 1) * vocab + x]) : 1.f;
+    // (a NaN is zero here, too)
+    s_d[tid] = drow && up >= -1 && in ? fmaxf(to_f32(drow[(int64_t)(up + 1) * vocab + x]), 0.f) : 1.f;
   }
   __syncthreads();
   if (CS > 1) cluster.barrier_wait();
