@@ -131,14 +131,14 @@ __device__ __forceinline__ int swizzle(int row) { return ((row & 6) ^ ((row & 1)
 template <typename T> struct Pair;
 template <> struct Pair<__nv_bfloat16> {
   uint32_t x = 0u;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { x = __ldg(reinterpret_cast<const uint32_t *>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { x = *reinterpret_cast<const uint32_t *>(p); }
   __device__ __forceinline__ float2 get() const {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
   }
 };
 template <> struct Pair<float> {
   float2 x = {0.f, 0.f};
-  __device__ __forceinline__ void load(const float *p) { x = __ldg(reinterpret_cast<const float2 *>(p)); }
+  __device__ __forceinline__ void load(const float *p) { x = *reinterpret_cast<const float2 *>(p); }
   __device__ __forceinline__ float2 get() const { return x; }
 };
 __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float a, float b) {
@@ -179,10 +179,10 @@ template <int DK, int DV, int NT, typename TIn> struct TreeCfg {
 
 template <int DK, int DV, int NT, typename TIn>
 __global__ void __launch_bounds__(TreeCfg<DK, DV, NT, TIn>::THREADS)
-decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
-                   const TIn *__restrict__ v, const float *__restrict__ g,
-                   const float *__restrict__ beta, const float *__restrict__ state,
-                   const int32_t *__restrict__ parents, TIn *__restrict__ out, int T, int H) {
+decode_tree_kernel(const TIn *q, const TIn *k,
+                   const TIn *v, const float *g,
+                   const float *beta, const float *state,
+                   const int32_t *parents, TIn *__restrict__ out, int T, int H) {
   using Cfg = TreeCfg<DK, DV, NT, TIn>;
   using Mask = typename MaskOf<NT>::T;
   constexpr bool X3 = Cfg::X3;
@@ -213,8 +213,8 @@ decode_tree_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
       up[e] = -2;
       bt[e] = 0.f;
       if (t < T) {
-        up[e] = parents ? __ldg(parents + (int64_t)n * T + t) : t - 1;
-        bt[e] = __ldg(beta + row0 + (int64_t)t * H);
+        up[e] = parents ? parents[(int64_t)n * T + t] : t - 1;
+        bt[e] = beta[row0 + (int64_t)t * H];
       }
     }
   }

@@ -197,10 +197,10 @@ template <int N> __device__ __forceinline__ bool bar_or(bool x) {
 
 template <int TP>
 __global__ void __launch_bounds__(TreeTc<TP>::THREADS, TP == 16 ? 2 : 1)
-decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
-                      const __nv_bfloat16 *__restrict__ v, const float *__restrict__ g,
-                      const float *__restrict__ beta, const float *__restrict__ state,
-                      const int32_t *__restrict__ parents, __nv_bfloat16 *__restrict__ out, int T,
+decode_tree_tc_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *k,
+                      const __nv_bfloat16 *v, const float *g,
+                      const float *beta, const float *state,
+                      const int32_t *parents, __nv_bfloat16 *__restrict__ out, int T,
                       int H, int32_t *dev_status, uint64_t wait_ns) {
   using C = TreeTc<TP>;
   extern __shared__ uint8_t smem_raw[];
@@ -281,8 +281,8 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         up[e] = -2;
         bt[e] = 0.f;
         if (t < T) {
-          up[e] = parents ? __ldg(parents + (int64_t)n * T + t) : t - 1;
-          bt[e] = __ldg(beta + row0 + (int64_t)t * H);
+          up[e] = parents ? parents[(int64_t)n * T + t] : t - 1;
+          bt[e] = beta[row0 + (int64_t)t * H];
         }
       }
 #pragma unroll

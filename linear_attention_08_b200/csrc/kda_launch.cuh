@@ -4,7 +4,9 @@
 // Such a kernel's blocks are started as soon as every block of the kernel ahead has
 // called launch_dependents() or ended; they set up their shared memory, and
 // wait_for_inputs() returns once the kernel ahead has completed and its writes are
-// visible.  No global memory is touched before that.  A kernel ahead that does not call
+// visible.  No global memory is touched before that, and inputs are read by ordinary loads:
+// __ldg and const pointers with __restrict__ promise memory that does not change while the
+// kernel runs, which what the kernel ahead writes does.  A kernel ahead that does not call
 // launch_dependents() has the usual order.  One user's calls in a row: tree decode 8.2 ->
 // 5.5 us, commit 8.2 -> 5.9 us.
 #pragma once

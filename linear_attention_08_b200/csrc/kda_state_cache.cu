@@ -91,6 +91,21 @@ __device__ __forceinline__ uint32_t encode4(float4 x, float scale, const Factor 
   return scale > 0.f ? encode4_exact<E4M3>(x, scale) : 0u;   // false for a NaN scale too
 }
 
+// Read once, behind the wait for the kernel ahead.
+__device__ __forceinline__ float4 load_once(const float4 *p) {
+  float4 x;
+  asm volatile("ld.global.cs.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "l"(p)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t load_once(const uint32_t *p) {
+  uint32_t x;
+  asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+
 template <bool E4M3> __device__ __forceinline__ float4 decode4(uint32_t c, float scale) {
   float4 x;
   if (E4M3) {
@@ -107,7 +122,7 @@ template <bool E4M3> __device__ __forceinline__ float4 decode4(uint32_t c, float
 
 template <int DK, int DV, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads, 3)
-state_store_kernel(const float *__restrict__ states, const int32_t *__restrict__ slots,
+state_store_kernel(const float *states, const int32_t *slots,
                    uint32_t *__restrict__ cache, float *__restrict__ scales, int N, int H,
                    int64_t num_slots) {
   constexpr int V4 = DV / 4;                          // lanes of one row
@@ -124,7 +139,7 @@ state_store_kernel(const float *__restrict__ states, const int32_t *__restrict__
   const float4 *src = reinterpret_cast<const float4 *>(states) + unit * (DK * V4);
   float4 x[ITER];
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) x[i] = __ldcs(src + (rg + i * RPP) * V4 + cg);
+  for (int i = 0; i < ITER; ++i) x[i] = load_once(src + (rg + i * RPP) * V4 + cg);
   // A slot named twice keeps the last entry's state, whichever CTA runs first.
   int later = 0;
   for (int j = n + 1 + tid; j < N; j += kCacheThreads) later |= slots[j] == slot;
@@ -152,8 +167,8 @@ state_store_kernel(const float *__restrict__ states, const int32_t *__restrict__
 
 template <int DK, int DV, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads)
-state_load_kernel(const uint32_t *__restrict__ cache, const float *__restrict__ scales,
-                  const int32_t *__restrict__ slots, float *__restrict__ states, int H,
+state_load_kernel(const uint32_t *cache, const float *scales,
+                  const int32_t *slots, float *__restrict__ states, int H,
                   int64_t num_slots) {
   constexpr int V4 = DV / 4;
   constexpr int RPP = kCacheThreads / V4;
@@ -177,7 +192,7 @@ state_load_kernel(const uint32_t *__restrict__ cache, const float *__restrict__ 
   uint32_t c[ITER];
   float s[ITER];
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) c[i] = __ldcs(src + (rg + i * RPP) * V4 + cg);
+  for (int i = 0; i < ITER; ++i) c[i] = load_once(src + (rg + i * RPP) * V4 + cg);
 #pragma unroll
   for (int i = 0; i < ITER; ++i) s[i] = sc[rg + i * RPP];
 #pragma unroll

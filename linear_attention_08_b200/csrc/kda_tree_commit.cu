@@ -81,10 +81,10 @@ __device__ __forceinline__ int nth(unsigned long long path, int j) {
 
 template <int DK, int DV, typename TIn>
 __global__ void __launch_bounds__(CommitCfg<DK, DV, TIn>::THREADS, CommitCfg<DK, DV, TIn>::PER_SM)
-tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
-                   const float *__restrict__ g, const float *__restrict__ beta,
-                   const float *state, float *state_out, const int32_t *__restrict__ parents,
-                   const int32_t *__restrict__ accept_node, int T, int H, int64_t items) {
+tree_commit_kernel(const TIn *k, const TIn *v,
+                   const float *g, const float *beta,
+                   const float *state, float *state_out, const int32_t *parents,
+                   const int32_t *accept_node, int T, int H, int64_t items) {
   using C = CommitCfg<DK, DV, TIn>;
   constexpr int COLS = C::COLS, PARTS = C::PARTS, THREADS = C::THREADS, ROWS = C::ROWS;
   constexpr int V4 = DV / 4;
@@ -106,10 +106,10 @@ tree_commit_kernel(const TIn *__restrict__ k, const TIn *__restrict__ v,
   const auto read_ahead = [&](int64_t item) {
     if (item >= items) return;
     const int64_t n = item / PARTS / H;
-    node = __ldg(accept_node + n);
+    node = accept_node[n];
     if (parents) {
-      if (lane < T) up0 = __ldg(parents + n * T + lane);
-      if (lane + 32 < T) up1 = __ldg(parents + n * T + lane + 32);
+      if (lane < T) up0 = parents[n * T + lane];
+      if (lane + 32 < T) up1 = parents[n * T + lane + 32];
     }
   };
   // The path as a set of places, found by every warp for itself.

@@ -66,7 +66,7 @@ __device__ __forceinline__ double scaled_bf16(uint32_t bits) {   // of the upper
 template <typename P, int W> struct Raw;
 template <> struct Raw<float, 4> {
   uint4 x;
-  __device__ __forceinline__ void load(const float *p) { x = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void load(const float *p) { x = *reinterpret_cast<const uint4 *>(p); }
   __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(double (&f)[4]) const {
     f[0] = scaled(__uint_as_float(x.x)); f[1] = scaled(__uint_as_float(x.y));
@@ -76,7 +76,7 @@ template <> struct Raw<float, 4> {
 template <> struct Raw<__nv_bfloat16, 8> {
   uint4 x;
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-    x = __ldg(reinterpret_cast<const uint4 *>(p));
+    x = *reinterpret_cast<const uint4 *>(p);
   }
   __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(double (&f)[8]) const {
@@ -90,7 +90,7 @@ template <> struct Raw<__nv_bfloat16, 8> {
 };
 template <typename P> struct Raw<P, 1> {
   P x;
-  __device__ __forceinline__ void load(const P *p) { x = __ldg(p); }
+  __device__ __forceinline__ void load(const P *p) { x = *p; }
   __device__ __forceinline__ void clear() { x = from_f32<P>(0.f); }
   __device__ __forceinline__ void get(double (&f)[1]) const { f[0] = scaled(to_f32(x)); }
 };
@@ -238,9 +238,9 @@ __device__ __forceinline__ int find_part(double mine, double base, double border
 
 template <typename P>
 __global__ void __launch_bounds__(kVThreads, 2)
-verify_tree_kernel(const P *__restrict__ target, const P *__restrict__ draft,
-                   const int32_t *__restrict__ tokens, const int32_t *__restrict__ parents,
-                   const float *__restrict__ uniforms, int32_t *__restrict__ accept_node,
+verify_tree_kernel(const P *target, const P *draft,
+                   const int32_t *tokens, const int32_t *parents,
+                   const float *uniforms, int32_t *__restrict__ accept_node,
                    int32_t *__restrict__ accept_len, int32_t *__restrict__ out_tokens, int T,
                    int vocab) {
   __shared__ int32_t s_tok[kVMaxNodes], s_par[kVMaxNodes], s_path[kVMaxNodes], s_gone[kVMaxNodes];
