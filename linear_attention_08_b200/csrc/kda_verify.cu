@@ -62,11 +62,26 @@ __device__ __forceinline__ double scaled_bf16(uint32_t bits) {   // of the upper
   return __hiloint2double((int)(__float_as_uint(fmaxf(__uint_as_float(bits), 0.f)) >> 3), 0);
 }
 
+// 16 bytes, or an element, of global memory (which a called function does not know p to be in).
+__device__ __forceinline__ uint4 load16(const void *p) {
+  uint4 x;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ void load1(const float *p, float &x) {
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(x) : "l"(p));
+}
+__device__ __forceinline__ void load1(const __nv_bfloat16 *p, __nv_bfloat16 &x) {
+  unsigned short b;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(b) : "l"(p));
+  x = __ushort_as_bfloat16(b);
+}
+
 // W neighbouring elements as one load gives them (one, or 16 bytes), and their values.
 template <typename P, int W> struct Raw;
 template <> struct Raw<float, 4> {
   uint4 x;
-  __device__ __forceinline__ void load(const float *p) { x = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void load(const float *p) { x = load16(p); }
   __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(double (&f)[4]) const {
     f[0] = scaled(__uint_as_float(x.x)); f[1] = scaled(__uint_as_float(x.y));
@@ -75,9 +90,7 @@ template <> struct Raw<float, 4> {
 };
 template <> struct Raw<__nv_bfloat16, 8> {
   uint4 x;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-    x = *reinterpret_cast<const uint4 *>(p);
-  }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { x = load16(p); }
   __device__ __forceinline__ void clear() { x = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(double (&f)[8]) const {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -90,7 +103,7 @@ template <> struct Raw<__nv_bfloat16, 8> {
 };
 template <typename P> struct Raw<P, 1> {
   P x;
-  __device__ __forceinline__ void load(const P *p) { x = *p; }
+  __device__ __forceinline__ void load(const P *p) { load1(p, x); }
   __device__ __forceinline__ void clear() { x = from_f32<P>(0.f); }
   __device__ __forceinline__ void get(double (&f)[1]) const { f[0] = scaled(to_f32(x)); }
 };
