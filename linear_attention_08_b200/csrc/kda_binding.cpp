@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "kda.h"
@@ -273,8 +274,8 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
   try {
     return F(a, n);
   } catch (const Refused &) {
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {          // as PyTorch's own functions raise it (memory that is not there, ...)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
