@@ -364,6 +364,9 @@ def _native():
         except ImportError as e:
             raise ImportError("_binding.so is missing or does not fit this PyTorch: build it with "
                               f"`python -m linear_attention_08_b200.build` ({e})") from e
+        if _binding.torch_version != str(torch.__version__):
+            raise ImportError(f"_binding.so was built for PyTorch {_binding.torch_version}, this is {torch.__version__}: "
+                              "build it again with `python -m linear_attention_08_b200.build`")
         _native_module = _binding
     return _native_module
 
