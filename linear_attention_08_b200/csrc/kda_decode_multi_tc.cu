@@ -400,10 +400,12 @@ decode_multi_tc_kernel(const __grid_constant__ MtcMaps maps, const float *__rest
     }
     tc::fence_smem_to_async();
     tc::fence_before_sync();
-    __syncthreads();
+    // Every thread has read the accepted length for itself, and a caller who rewrites it while
+    // the kernel runs makes them disagree; what barriers depend on is decided together.
+    const bool keep = __syncthreads_or(a >= 0);
 
     // ---- acc2 += V_new^T Khat; the state out (a warp writes 128 consecutive bytes) ----
-    if (a >= 0) {
+    if (keep) {
       if (tid == 0) {
         tc::fence_after_sync();
         tc::mma_bf16(tmem + kAcc2, tc::desc_mnmajor(sb + Lay::A2, 16, 0),
