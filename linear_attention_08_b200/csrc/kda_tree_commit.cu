@@ -184,65 +184,67 @@ tree_commit_kernel(const TIn *k, const TIn *v,
     for (int e = tid; e < m * COLS; e += THREADS)
       s_v[e / COLS][e % COLS] = to_f32(reinterpret_cast<const TIn *>(&s_raw[e / COLS][C::CG + C::CK])[e % COLS]);
     if (tid < m) s_b[tid] = s_rb[tid];
-    __syncthreads();
+    // Every warp has read the path for itself, and a caller who rewrites accept_node or parents
+    // while the kernel runs makes them disagree; what barriers depend on is decided together.
+    bool more = __syncthreads_or(__popcll(path) > kGroup);
     if (next < items) {
       if (!in_place || next_path != 0) start_state(next);
       start_rows(next, next_path);
     }
-    if (active) {
-      while (m > 0) {
-        for (int j = 0; j < m; ++j) {
-          f32x2 ya = 0, yb = 0;
+    for (;;) {
+      for (int j = 0; j < m; ++j) {
+        f32x2 ya = 0, yb = 0;
 #pragma unroll
-          for (int i = 0; i < ROWS; ++i) {
-            const ulonglong2 ak = *reinterpret_cast<const ulonglong2 *>(&s_ak[j][ks + 8 * i]);
-            s[i].x = mul2(s[i].x, ak.x);
-            s[i].y = mul2(s[i].y, ak.x);
-            ya = fma2(ak.y, s[i].x, ya);
-            yb = fma2(ak.y, s[i].y, yb);
-          }
-          const float2 y01 = unpack2(ya), y23 = unpack2(yb);
-          const float4 y = make_float4(y01.x, y01.y, y23.x, y23.y);
-          // Sum over the 8 row residues: each step halves the columns a lane
-          // keeps, so a lane ends with one column (7 shuffles, not 12).
-          const bool b4 = lane & 16, b3 = lane & 8;
-          float p0 = b4 ? y.z : y.x, p1 = b4 ? y.w : y.y;
-          p0 += __shfl_xor_sync(0xffffffffu, b4 ? y.x : y.z, 16);
-          p1 += __shfl_xor_sync(0xffffffffu, b4 ? y.y : y.w, 16);
-          float w = b3 ? p1 : p0;
-          w += __shfl_xor_sync(0xffffffffu, b3 ? p0 : p1, 8);
-          w += __shfl_xor_sync(0xffffffffu, w, 4);
-          const float u = s_b[j] * (s_v[j][4 * cg + (b4 ? 2 : 0) + (b3 ? 1 : 0)] - w);
-          const float u8 = __shfl_xor_sync(0xffffffffu, u, 8);
-          const float ua = b3 ? u8 : u, ub = b3 ? u : u8;
-          const float ua16 = __shfl_xor_sync(0xffffffffu, ua, 16);
-          const float ub16 = __shfl_xor_sync(0xffffffffu, ub, 16);
-          const f32x2 u01 = b4 ? pack2(ua16, ub16) : pack2(ua, ub);
-          const f32x2 u23 = b4 ? pack2(ua, ub) : pack2(ua16, ub16);
+        for (int i = 0; i < ROWS; ++i) {
+          const ulonglong2 ak = *reinterpret_cast<const ulonglong2 *>(&s_ak[j][ks + 8 * i]);
+          s[i].x = mul2(s[i].x, ak.x);
+          s[i].y = mul2(s[i].y, ak.x);
+          ya = fma2(ak.y, s[i].x, ya);
+          yb = fma2(ak.y, s[i].y, yb);
+        }
+        const float2 y01 = unpack2(ya), y23 = unpack2(yb);
+        const float4 y = make_float4(y01.x, y01.y, y23.x, y23.y);
+        // Sum over the 8 row residues: each step halves the columns a lane
+        // keeps, so a lane ends with one column (7 shuffles, not 12).
+        const bool b4 = lane & 16, b3 = lane & 8;
+        float p0 = b4 ? y.z : y.x, p1 = b4 ? y.w : y.y;
+        p0 += __shfl_xor_sync(0xffffffffu, b4 ? y.x : y.z, 16);
+        p1 += __shfl_xor_sync(0xffffffffu, b4 ? y.y : y.w, 16);
+        float w = b3 ? p1 : p0;
+        w += __shfl_xor_sync(0xffffffffu, b3 ? p0 : p1, 8);
+        w += __shfl_xor_sync(0xffffffffu, w, 4);
+        const float u = s_b[j] * (s_v[j][4 * cg + (b4 ? 2 : 0) + (b3 ? 1 : 0)] - w);
+        const float u8 = __shfl_xor_sync(0xffffffffu, u, 8);
+        const float ua = b3 ? u8 : u, ub = b3 ? u : u8;
+        const float ua16 = __shfl_xor_sync(0xffffffffu, ua, 16);
+        const float ub16 = __shfl_xor_sync(0xffffffffu, ub, 16);
+        const f32x2 u01 = b4 ? pack2(ua16, ub16) : pack2(ua, ub);
+        const f32x2 u23 = b4 ? pack2(ua, ub) : pack2(ua16, ub16);
 #pragma unroll
-          for (int i = 0; i < ROWS; ++i) {
-            const f32x2 kc = reinterpret_cast<const ulonglong2 *>(&s_ak[j][ks + 8 * i])->y;
-            s[i].x = fma2(kc, u01, s[i].x);
-            s[i].y = fma2(kc, u23, s[i].y);
-          }
+        for (int i = 0; i < ROWS; ++i) {
+          const f32x2 kc = reinterpret_cast<const ulonglong2 *>(&s_ak[j][ks + 8 * i])->y;
+          s[i].x = fma2(kc, u01, s[i].x);
+          s[i].y = fma2(kc, u23, s[i].y);
         }
-        // the path's further tokens, read when they are needed
-        for (int j = 0; j < m; ++j) path &= path - 1;
-        m = min(kGroup, __popcll(path));
-        if (m == 0) break;
-        const int64_t row0 = first_row(item);
-        __syncthreads();
-        for (int e = tid; e < m * (DK + COLS); e += THREADS) {
-          const int j = e / (DK + COLS), c = e % (DK + COLS);
-          const int64_t row = row0 + (int64_t)nth(path, j) * H;
-          if (c < DK) {
-            const float al = expf(g[row * DK + c]), kc = to_f32(k[row * DK + c]);
-            s_ak[j][c] = make_float4(al, al, kc, kc);
-          } else s_v[j][c - DK] = to_f32(v[row * DV + item % PARTS * COLS + (c - DK)]);
-          if (c == 0) s_b[j] = beta[row];
-        }
-        __syncthreads();
       }
+      // the path's further tokens, read when they are needed
+      if (!more) break;
+      for (int j = 0; j < m; ++j) path &= path - 1;
+      m = min(kGroup, __popcll(path));
+      const int64_t row0 = first_row(item);
+      __syncthreads();
+      for (int e = tid; e < m * (DK + COLS); e += THREADS) {
+        const int j = e / (DK + COLS), c = e % (DK + COLS);
+        const int64_t row = row0 + (int64_t)nth(path, j) * H;
+        if (c < DK) {
+          const float al = expf(g[row * DK + c]), kc = to_f32(k[row * DK + c]);
+          s_ak[j][c] = make_float4(al, al, kc, kc);
+        } else s_v[j][c - DK] = to_f32(v[row * DV + item % PARTS * COLS + (c - DK)]);
+        if (c == 0) s_b[j] = beta[row];
+      }
+      more = __syncthreads_or(__popcll(path) > kGroup);
+    }
+    if (active) {
       float4 *dst = reinterpret_cast<float4 *>(state_out) + elements(item);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {

@@ -16,3 +16,12 @@ def test_multi_token_decode_decides_together():
     loop = text[text.index("for (; u < units; u += G)"):]
     assert "const bool keep = __syncthreads_or(a >= 0);" in loop
     assert not re.search(r"if \(a [<>=]+ 0\)", loop)      # (selects of values are fine)
+
+
+def test_commit_decides_together():
+    text = source("kda_tree_commit.cu")
+    loop = text[text.index("for (; item < items; item += G)"):]
+    assert loop.count("more = __syncthreads_or(__popcll(path) > kGroup);") == 2
+    steps = loop[loop.index("for (;;) {"):loop.index("float4 *dst")]
+    assert steps.count("__syncthreads") == 2 and re.search(r"if \(!more\) break;", steps)
+    assert "if (active)" in steps and "if (active)" not in steps[:steps.rindex("__syncthreads_or")]
