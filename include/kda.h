@@ -269,9 +269,11 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const f
  * outside the preconditions: they leave the outputs of the tokens that follow
  * them not finite, perhaps those of other branches of the same sequence and head,
  * and no others.  FP32 inputs give FP32 accuracy; BF16 inputs run the products in
- * TF32, below the rounding of out.  BF16 with D_k = D_v = 128 runs on the tensor
- * cores with the state in tensor memory (its waits are bounded, dev_status tells
- * of one that ran out); other shapes run warp-level tensor products.
+ * TF32, below the rounding of out, for states and rows of magnitudes up to 10^31
+ * (BF16 rows converted to FP32 give FP32 products and an FP32 out).  BF16 with
+ * D_k = D_v = 128 runs on the tensor cores with the state in tensor memory (its
+ * waits are bounded, dev_status tells of one that ran out); other shapes run
+ * warp-level tensor products.
  *
  * kda_tree_commit: state_out = the state after place accept_node[n], by the
  * recurrence in FP32 along its path.  A value outside [0, nodes_per_seq), or an

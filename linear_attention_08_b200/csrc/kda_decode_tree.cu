@@ -13,7 +13,8 @@
 //
 // L and P are the gated products with exp(Gam_t - Gam_s), which is at most one;
 // the factors exp(-Gam_s) alone are not, so a unit whose Kh leaves 10^36 or whose
-// Gam leaves +-80 forms L and P pair by pair from the differences instead.
+// Gam leaves +-80 forms L and P pair by pair from the differences instead (deep trees with
+// gates near -5; 128 x 32 heads x 61 places, D = 64 in BF16: 989 us instead of 209).
 //
 // Layout: one CTA per (sequence, head).  Everything is computed transposed,
 // O^T = S0^T Qt^T + Vn^T P^T, with value columns as the rows of m16n8k8 products:
@@ -29,13 +30,13 @@
 // sizes, and FP32, whose three products per product the warp-level instructions take
 // with operands split in registers.  It is bound by issue slots and by the round trips
 // to memory (parents, then all rows at once): 512 x 32 heads x 16 places of D = 64 in
-// BF16 take 132 us against 72 at the copy rate, of D = 128 in FP32 618 against 267.
+// BF16 take 132 us against 72 at the copy rate, of D = 128 in FP32 617 against 267.
 //
 // Arithmetic: TF32 products with FP32 accumulation for BF16 inputs (operands are
-// rounded to about the nearest, 2^-11.7 of a value rms, against 2^-9 when out is
-// rounded).  FP32
-// inputs split each operand in two TF32 terms and add three products, and carry
-// Gam as an unevaluated sum of two FP32 numbers, for FP32 accuracy.
+// rounded to about the nearest, 2^-10.5 of a value at most and 2^-11.7 rms, against
+// 2^-9 when out is rounded).  FP32 inputs split each operand in two TF32 terms and add
+// three products, and carry Gam as an unevaluated sum of two FP32 numbers, for FP32
+// accuracy.
 #include "kda_common.cuh"
 #include "kda_launch.cuh"
 
@@ -157,10 +158,11 @@ template <> struct MaskOf<8> { using T = unsigned long long; };
 template <int DK, int DV, int NT, typename TIn> struct TreeCfg {
   static constexpr bool X3 = sizeof(TIn) == 4;
   static constexpr int WARPS = DV / 16;             // 16 value columns each, two per lane
-  // Rows are loaded into registers as soon as the paths are known, all at once (512 x 32
-  // heads x 16 places of D = 64, BF16: 147 us, 223 when they were loaded where they are
-  // used; 128 x 32 x 61 places: 218 and 396), except where the registers cost the second
-  // CTA of an SM (FP32, 256 x 32 x 30 places, D = 64/128: 629 us, 577 without).
+  // Rows are loaded into registers as soon as the paths are known, all at once (before the
+  // operands' rounding was a product, 512 x 32 heads x 16 places of D = 64, BF16: 147 us, 223
+  // when they were loaded where they are used; 128 x 32 x 61 places: 218 and 396), except
+  // where the registers cost the second CTA of an SM (FP32, 256 x 32 x 30 places: D = 64/128
+  // 542 us, 512 without; 32/128 445 and 437).
   static constexpr bool AHEAD = !(X3 && NT == 4 && WARPS == 8 && DK < 128);
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int T8 = 8 * NT;
@@ -557,8 +559,9 @@ decode_tree_kernel(const TIn *q, const TIn *k,
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         // The conversion instruction is slower than the product of operand(), but with 64
-        // elements per lane the code around it comes out faster (512 x 32 heads x 16
-        // places, BF16: D = 128/64 243 us against 310; D = 64/128 309 against 252).
+        // elements per lane the code around it comes out no slower, and faster for four tiles
+        // of places (256 x 32 heads x 30 places, BF16: D = 128/32 276 us against 312, 128/64
+        // 250 both; 512 x 32 x 16: 128/32 213 against 211, 64/128 309 against 252).
         float &x = s0[4 * a + m][e];
         x = !X3 && DK == 128 ? rn_tf32(x) : operand<X3>(x);
       }

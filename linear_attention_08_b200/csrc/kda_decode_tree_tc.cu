@@ -25,9 +25,14 @@
 //
 // One CTA per unit is launched, and a CTA that runs takes over those that have not
 // started (launch control): units of ragged trees differ in cost by a factor of two.
-// TP = 16: two CTAs of 128 + 32 threads per SM, so that one
-// computes while the other waits for a product.  TP = 32, 64: the buffers allow one CTA,
-// of 256 + 32 threads; X holds 32 tokens, and the second 32 take the place of g.
+// TP = 16: two CTAs of 128 + 32 threads per SM, so that one computes while the other waits
+// for a product.  TP = 32, 64: these buffers leave room for one CTA, of 256 + 32 threads; X
+// holds 32 tokens, and the second 32 take the place of g.
+//
+// 512 x 32 heads x 16 places: 237 us in a burst, 226 at the copy rate (264 to 288 under the
+// power cap).  Units whose decays leave +-80 form KK and P pair by pair (deep trees with
+// gates near -5), which is what they then spend their time on: 128 x 32 heads x 61 places
+// 1525 us instead of 259.
 #include "kda_common.cuh"
 #include "kda_launch.cuh"
 #include "kda_tc_util.cuh"
@@ -197,11 +202,10 @@ template <int N> __device__ __forceinline__ bool bar_or(bool x) {
 
 template <int TP>
 __global__ void __launch_bounds__(TreeTc<TP>::THREADS, TP == 16 ? 2 : 1)
-decode_tree_tc_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *k,
-                      const __nv_bfloat16 *v, const float *g,
-                      const float *beta, const float *state,
-                      const int32_t *parents, __nv_bfloat16 *__restrict__ out, int T,
-                      int H, int32_t *dev_status, uint64_t wait_ns) {
+decode_tree_tc_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
+                      const float *g, const float *beta, const float *state,
+                      const int32_t *parents, __nv_bfloat16 *__restrict__ out, int T, int H,
+                      int32_t *dev_status, uint64_t wait_ns) {
   using C = TreeTc<TP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sraw = smem_u32(smem_raw);

@@ -17,8 +17,8 @@
 // barrier), takes them into registers when the unit begins, and starts the next
 // unit's copies into the same slots.  accept_node and parents are read two units
 // ahead, the path's first rows one unit ahead.  (Without this a CTA waited in turn
-// for accept_node, the state and the rows: 512 x 32 units in 416 us; 351 with it, 95 %
-// of the copy rate.)
+// for accept_node, the state and the rows: 512 x 32 units in 416 us.  With it 354, 94 %
+// of the copy rate, in a burst; 366 to 384 under the power cap.)
 #include "kda_common.cuh"
 #include "kda_launch.cuh"
 
@@ -81,8 +81,7 @@ __device__ __forceinline__ int nth(unsigned long long path, int j) {
 
 template <int DK, int DV, typename TIn>
 __global__ void __launch_bounds__(CommitCfg<DK, DV, TIn>::THREADS, CommitCfg<DK, DV, TIn>::PER_SM)
-tree_commit_kernel(const TIn *k, const TIn *v,
-                   const float *g, const float *beta,
+tree_commit_kernel(const TIn *k, const TIn *v, const float *g, const float *beta,
                    const float *state, float *state_out, const int32_t *parents,
                    const int32_t *accept_node, int T, int H, int64_t items) {
   using C = CommitCfg<DK, DV, TIn>;

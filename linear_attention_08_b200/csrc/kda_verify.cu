@@ -13,11 +13,11 @@
 // r(0) + ... + r(j) > u_last sum(r).  (r / R is what is left of the target's
 // distribution; the test and the draw do not change when r and R are scaled
 // together, so r is not divided by R, and may double with every refusal:
-// a + |a| = 2 max(a, 0) is one FP64 addition, a maximum four instructions.)  Accepted and drawn tokens then follow the
-// target's distribution exactly, for one drafted token per context (a chain)
-// and for several drawn from d_c (a tree).  Without a draft distribution (tokens
-// from a lookup, not a sample) d_c is one at the token itself: a refusal sets
-// r(x) = 0 and takes p_c(x) from R.
+// a + |a| = 2 max(a, 0) is one FP64 addition, a maximum four instructions.)
+// Accepted and drawn tokens then follow the target's distribution exactly, for
+// one drafted token per context (a chain) and for several drawn from d_c (a
+// tree).  Without a draft distribution (tokens from a lookup, not a sample) d_c
+// is one at the token itself: a refusal sets r(x) = 0 and takes p_c(x) from R.
 //
 // Sums and comparisons are FP64: a token's border in the cumulative sum has to come
 // out the same whatever order the sum is taken in, and FP32 would move one draw in
@@ -33,6 +33,10 @@
 // their sums over distributed shared memory, and the CTA whose slice holds the
 // border finds the token.  No atomics and no workspace: the result does not
 // depend on scheduling, and calls on any streams do not share anything.
+//
+// 64 chains of 7 tokens, 131072 BF16 elements: 14.0 us, 5.1 at the copy rate; without a
+// draft 12.2.  48 trees of 24 places, 50257 FP32 elements: 19 to 24 us (the sequence with
+// most refusals sets the time), 3.0 at the copy rate; without a draft 14.5.
 #include <cooperative_groups.h>
 
 #include "kda_common.cuh"
