@@ -39,6 +39,7 @@
 // accuracy.
 #include "kda_common.cuh"
 #include "kda_launch.cuh"
+#include "kda_tf32.cuh"
 
 namespace kda {
 namespace {

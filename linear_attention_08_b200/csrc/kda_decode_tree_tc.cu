@@ -36,6 +36,7 @@
 #include "kda_common.cuh"
 #include "kda_launch.cuh"
 #include "kda_tc_util.cuh"
+#include "kda_tf32.cuh"
 #include "kda_tma.cuh"
 
 namespace kda {

@@ -29,6 +29,7 @@
 
 #include "kda_common.cuh"
 #include "kda_launch.cuh"
+#include "kda_tf32.cuh"
 
 namespace kda {
 namespace {
