@@ -38,8 +38,8 @@ cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
-  const cudaError_t last = cudaGetLastError();   // (a failure does not stay for the next check)
-  return e != cudaSuccess ? e : last;
+  if (e != cudaSuccess) cudaGetLastError();   // does not stay for the next check
+  return e;                                    // (not an error that an earlier call left)
 }
 
 }  // namespace kda
